@@ -332,6 +332,114 @@ int lsa_hot_pool_update(int B, int N, int slots, size_t row_bytes, uint32_t trig
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * The 8-bit KV cache -- rows of compressed KV entries or of tokens held as e4m3 codes, the
+ * cache that a decode step writes, fetches from and attends over ([SUMMARY] §2.1: the
+ * fetched entries are what the backbone's attention then reads; [REVIEW] 四: the KV
+ * cache is what the method shrinks).  The pages do not give a storage format; the one
+ * taken:
+ *   rows  [pages][page][G][W] uint8: page p holds `page` tokens (a power of two), a token
+ *         has G KV heads' rows of W codes (W a multiple of 16).
+ *   scale [B][ceil(N/block)][G] fp32: one scale for each `block` consecutive tokens (a
+ *         power of two, 1 to 128) of a sequence and each head; value = code * scale.
+ *   table [B][ceil(N/page)] int32 or NULL: token t of sequence b lies in page
+ *         b * seq_pages + table[b][t / page] (NULL: b * seq_pages + t / page), at place
+ *         t mod page.  seq_pages = 0: one pool for all sequences; else a sequence's page
+ *         numbers are below seq_pages.  A negative number: not resident.
+ * With page = 1 and seq_pages = slots the table is the slot_of array of the hot pool, whose
+ * rows (row_bytes = G * W) lsa_hot_pool_update fetches in half the bytes of bf16 rows; with
+ * G = 1, page = block = 1 and no table, rows and scale are a K_IComp array and its kscale.
+ * pages * page * G < 2^31.  A page number outside the pool is treated as not resident.
+ *
+ * lsa_kv_write -- quantises new tokens' rows into the cache.  Sequence b's new tokens are
+ * start[b] + i, i < count[b] (all T when count is NULL; at most T).  For each block of
+ * tokens and head, with amax the largest magnitude among its new tokens:
+ *     s = the smallest power of two with amax / s <= 448, at least 2^-24;
+ *     code = e4m3(x / s), rounded to nearest even.
+ * A block that holds earlier tokens of the sequence (below start[b]) keeps the larger of its
+ * old and the new scale; when that grows, its earlier codes become e4m3(code * s_old / s)
+ * (exact unless they fall among the type's subnormals).  Tokens behind the new ones keep
+ * their codes.  A block with a NaN or infinity gets the scale NaN and codes 0.
+ *   x: xdt (LSA_F32 or LSA_BF16), token (b, i) at element (b*T + i) * x_stride, [G][W] dense;
+ *   16-byte aligned, x_stride a multiple of 16 bytes.  start, count [B] int32.
+ *   Tokens outside [0, N) or not resident are skipped and raise *status (int32 or NULL) to
+ *   LSA_ERR_RANGE.  No two sequences may write the same page or share a partly filled block's
+ *   pages.  One launch.  B * T * G < 2^30.
+ *
+ * lsa_kv_read -- reads tokens back: out[b][j] = the values [G][W] of token idx[b][j] (token j
+ * itself when idx is NULL, then cap <= N), j < count[b] (all cap when count is NULL).
+ *   odt LSA_F32 (exact) or LSA_BF16 (rounded to nearest even); out [B][cap][G][W], 16-byte
+ *   aligned.  Negative entries are padding: their rows of out, and rows from count[b] on, are
+ *   left as they were.  Tokens outside [0, N) or not resident likewise, raising *status to
+ *   LSA_ERR_RANGE.  One launch.
+ * ---------------------------------------------------------------------------------- */
+int lsa_kv_write(int B, int T, int N, int G, int W, int xdt, const void* x, size_t x_stride, const int32_t* start,
+                 const int32_t* count, int block, int page, int seq_pages, int pages, const int32_t* table,
+                 void* rows, float* scale, int32_t* status, void* stream);
+
+int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const int32_t* count, int block, int page,
+                int seq_pages, int pages, const int32_t* table, const void* rows, const float* scale, int odt,
+                void* out, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * lsa_kv_attend -- attention over the 8-bit KV cache: the step that the selection prepares
+ * ([SUMMARY] §2.1 hierarchical selection: attention runs on the top-k entries inside the
+ * fetched subset).  Query token i (0 <= i < Tq) of sequence b has position
+ * p = length[b] - Tq + i; length[b] counts the cached tokens, the query tokens' own among
+ * them.  Head h reads KV head h / (H/G).  It sees
+ *   - the tokens t <= p with t < sinks or t > p - window (window < 0: every t <= p), and
+ *   - the entries e = idx[b][j], j < min(count[b], cap), 0 <= e < length[b], that are not
+ *     among those (idx NULL: none); an entry listed twice counts twice.
+ * With K_t the first d values and V_t the values [voff, voff + dv) of token t's row:
+ *     a_t = sm_scale * q . K_t;   out = sum_t softmax(a)_t V_t;   lse = ln sum_t exp(a_t).
+ * A query that sees nothing gets out = 0 and lse = -infinity.  Latent rows have keys and
+ * values in the same columns (voff = 0); rows with separate parts have voff = d.
+ *   q [B][Tq][H][d] and out [B][Tq][H][dv]: qdt (LSA_F32 or LSA_BF16); length, count [B]
+ *   int32; lse [B][Tq][H] fp32 or NULL; 0 <= length[b] <= N (clamped).
+ *   Negative list entries are padding (as lsa_topk leaves them).  Entries at or past
+ *   length[b], and visible tokens that are not resident, are skipped and raise *status to
+ *   LSA_ERR_RANGE.  A token whose scale is NaN makes the queries that see it NaN; other
+ *   codes and scales must be finite (codes 0x7f and 0xff are not written by lsa_kv_write).
+ *   d <= 576, dv <= 512, voff + dv <= 1024, H a multiple of G, B*Tq*H <= 2^24,
+ *   Tq*H/G <= 65536, else LSA_ERR_UNSUPPORTED (or INVALID_ARG).
+ * workspace: lsa_kv_attend_workspace_bytes(...) bytes, 256-byte aligned; calls that may
+ *   overlap on the GPU need their own (calls captured into graphs that run at the same time too).
+ * ---------------------------------------------------------------------------------- */
+size_t lsa_kv_attend_workspace_bytes(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt,
+                                     int sinks, int window, int cap);
+
+int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt, const void* q,
+                  float sm_scale, const int32_t* length, int sinks, int window, const int32_t* idx, int cap,
+                  const int32_t* count, int block, int page, int seq_pages, int pages, const int32_t* table,
+                  const void* rows, const float* scale, void* out, float* lse, int32_t* status, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * lsa_rope -- rotary positions of `rot` columns of each head (the 64 rotary columns behind
+ * the 512 latent ones of a compressed row, or a query head's).  Pair i of a token at
+ * position pos[r] turns by a = pos[r] * freq[i]:
+ *     (u, v) -> mscale * (u cos a - v sin a, u sin a + v cos a),
+ * where (u, v) are columns (2i, 2i + 1) (half = 0, interleaved) or (i, i + rot/2) (half = 1).
+ * inverse = 1 turns by -a: the gradient of the input from the output's gradient.
+ *   x, out: dt (LSA_F32 or LSA_BF16); token r, head h at element r * token stride + h * head
+ *   stride from the pointer, which is at the first rotated column; strides at least rot.  out
+ *   may be x with the same strides (in place); other columns are not touched.  pos [R] int32;
+ *   freq [rot/2] fp64 (device), radians a position.  The angle is formed in fp64.
+ *   rot even, at most 1024; H * rot <= 2^24.  One launch.
+ *
+ * lsa_rope_frequencies -- fills the HOST array freq [rot/2] with base^(-2i/rot), scaled for a
+ * context `factor` times the original length by the published YaRN rule: pairs that turn more
+ * than `fast` times within `original` positions keep their frequency, pairs that turn less
+ * than `slow` times are divided by factor, those between blend linearly in i.  factor = 1: no
+ * scaling (original, fast and slow unused).  base > 1, factor >= 1, fast > slow > 0.
+ * ---------------------------------------------------------------------------------- */
+int lsa_rope(int R, int H, int rot, int half, int dt, const void* x, long long x_token, long long x_head,
+             const int32_t* pos, const double* freq, float mscale, int inverse, void* out, long long o_token,
+             long long o_head, void* stream);
+
+int lsa_rope_frequencies(int rot, double base, double factor, double original, double fast, double slow,
+                         double* freq);
+
+/* ------------------------------------------------------------------------------------
  * lsa_index_train_step -- loss and gradients of one indexer training step ([SUMMARY]
  * §2.3: K_IComp frozen, only the query-side projections trained, BCE combined with a
  * focal loss; §2.2: vote labels).  For P query positions of one indexer layer against N

@@ -11,6 +11,11 @@ LIB_PATH = os.path.join(_HERE, "liblsa.so")
 c_int, c_size_t, c_void_p, c_float, c_char_p = (ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p,
                                                 ctypes.c_float, ctypes.c_char_p)
 
+c_longlong, c_double = ctypes.c_longlong, ctypes.c_double
+
+# block, page, seq_pages, pages, table, rows, scale of the 8-bit KV cache's calls
+_KV_CACHE = [c_int] * 4 + [c_void_p] * 3
+
 # name -> (restype, argtypes), in the order of include/lsa.h
 SIGNATURES = {
     "lsa_status_string": (c_char_p, [c_int]),
@@ -47,6 +52,15 @@ SIGNATURES = {
     "lsa_hot_pool_reset": (c_int, [c_int, c_int, c_int, c_void_p, c_void_p]),
     "lsa_hot_pool_update": (c_int, [c_int, c_int, c_int, c_size_t, ctypes.c_uint32, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "lsa_kv_write": (c_int, [c_int] * 6 + [c_void_p, c_size_t, c_void_p, c_void_p] + _KV_CACHE + [c_void_p, c_void_p]),
+    "lsa_kv_read": (c_int, [c_int] * 4 + [c_void_p, c_int, c_void_p] + _KV_CACHE + [c_int, c_void_p, c_void_p,
+                                                                                 c_void_p]),
+    "lsa_kv_attend_workspace_bytes": (c_size_t, [c_int] * 13),
+    "lsa_kv_attend": (c_int, [c_int] * 10 + [c_void_p, c_float, c_void_p, c_int, c_int, c_void_p, c_int, c_void_p]
+                      + _KV_CACHE + [c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "lsa_rope": (c_int, [c_int] * 5 + [c_void_p, c_longlong, c_longlong, c_void_p, c_void_p, c_float, c_int, c_void_p,
+                                       c_longlong, c_longlong, c_void_p]),
+    "lsa_rope_frequencies": (c_int, [c_int] + [c_double] * 5 + [c_void_p]),
     "lsa_check_bounded_wait": (c_int, [ctypes.c_uint32, c_void_p, c_void_p]),
     "lsa_index_train_step_workspace_bytes": (c_size_t, [c_int] * 6),
     "lsa_index_train_step": (c_int, [c_int] * 7 + [c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_int,

@@ -1,0 +1,243 @@
+// Attention over the 8-bit KV cache on the CUDA cores, and the join of a sequence's parts.
+//
+// For a query column c (a query token and head of one KV head's group) over the visible
+// tokens t:  x_t = sm * scale_t * (q_c . k_t),  o_c = sum_t 2^(x_t log2 e - m) scale_t v_t / l_c,
+// l_c = sum_t 2^(x_t log2 e - m), with k and v the stored codes.  One pass: the running
+// maximum m, the sum l and the weighted values are rescaled when a tile raises m.
+//
+// This path serves fp32 queries (which the tensor cores would round) and row shapes the
+// tensor-core path declines; products, sums and statistics are fp32.  Tokens are split into
+// parts when there are few (sequence, KV head) units; the parts' unnormalised sums are joined
+// by the second kernel.
+#include <algorithm>
+
+#include "kv_common.cuh"
+
+namespace lsa {
+namespace {
+
+constexpr int kTile = 32;          // tokens of a tile: one per lane for the scores
+constexpr int kWarps = 4;
+constexpr int kCols = 2;           // columns of a warp
+constexpr int kBlockCols = kWarps * kCols;
+constexpr int kMaxVpl = 16;        // value columns per lane (dv <= 512)
+
+__device__ __forceinline__ void store_out(void* out, int qdt, size_t i, float v) {
+  if (qdt == LSA_F32) static_cast<float*>(out)[i] = v;
+  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+}
+
+__global__ void __launch_bounds__(kWarps * 32)
+kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
+  extern __shared__ float smem[];
+  const KvGeom& g = a.g;
+  const int pitch = rows_used | 1;                 // odd: a lane per token reads without conflicts
+  float* kv = smem;                                // [kTile][pitch] values without their scale
+  float* qs = kv + kTile * pitch;                  // [kBlockCols][d]
+  float* tsc = qs + kBlockCols * a.d;              // [kTile] scale
+  int* tt = reinterpret_cast<int*>(tsc + kTile);   // [kTile] token (or -1), bit 31 set for list entries
+  long long* trow = reinterpret_cast<long long*>(tt + kTile);   // [kTile] row (8-byte aligned: kTile and kBlockCols are even)
+  const int hg = a.H / g.G, ncol = a.Tq * hg;
+  long long u = blockIdx.x;
+  const int part = static_cast<int>(u % a.splits); u /= a.splits;
+  const int cb = static_cast<int>(u % col_blocks); u /= col_blocks;
+  const int head = static_cast<int>(u % g.G), b = static_cast<int>(u / g.G);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const KvSpan sp = kv_span(a, b);
+  const int tiles = (sp.total + kTile - 1) / kTile;
+  const int tile0 = static_cast<int>(static_cast<long long>(tiles) * part / a.splits);
+  const int tile1 = static_cast<int>(static_cast<long long>(tiles) * (part + 1) / a.splits);
+
+  for (int e = threadIdx.x; e < kBlockCols * a.d; e += blockDim.x) {
+    const int c = cb * kBlockCols + e / a.d;
+    float v = 0.f;
+    if (c < ncol) {
+      const size_t at = ((static_cast<size_t>(b) * a.Tq + c / hg) * a.H + head * hg + c % hg) * a.d + e % a.d;
+      v = a.qdt == LSA_F32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
+    }
+    qs[e] = v;
+  }
+  const int vpl = (a.dv + 31) / 32;
+  float acc[kCols][kMaxVpl], m[kCols], l[kCols];
+  int pos[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+    const int col = cb * kBlockCols + warp * kCols + c;
+    pos[c] = sp.len - a.Tq + min(col, ncol - 1) / hg;
+#pragma unroll
+    for (int k = 0; k < kMaxVpl; ++k) acc[c][k] = 0.f;
+  }
+  const float xs = a.sm * 1.44269504088896f;       // log2 e
+  for (int tile = tile0; tile < tile1; ++tile) {
+    __syncthreads();
+    if (threadIdx.x < kTile) {
+      const int v = tile * kTile + threadIdx.x;
+      bool main = false;
+      int t = v < sp.total ? kv_token(a, sp, b, v, main) : -1;
+      long long row = -1;
+      float s = 0.f;
+      if (t >= 0) {
+        row = kv_row(g, b, t);
+        if (row < 0) {
+          raise_status(a.status, LSA_ERR_RANGE);
+          t = -1;
+        } else {
+          s = __ldg(g.scale + kv_scale_at(g, b, t, head));
+        }
+      }
+      tsc[threadIdx.x] = s;
+      trow[threadIdx.x] = row;
+      tt[threadIdx.x] = t < 0 ? -1 : main ? t : static_cast<int>(0x80000000u | static_cast<uint32_t>(t));
+    }
+    __syncthreads();
+    const int vpr = rows_used / 16;
+    for (int i = threadIdx.x; i < kTile * vpr; i += blockDim.x) {
+      const int t = i / vpr, v = i - t * vpr;
+      const long long row = trow[t];
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (row >= 0) c = __ldg(reinterpret_cast<const uint4*>(g.rows + (static_cast<size_t>(row) * g.G + head) * g.W) + v);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      float* dst = kv + t * pitch + v * 16;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) dst[k] = e4m3_to_float(static_cast<uint8_t>(w[k / 4] >> (8 * (k % 4))));
+    }
+    __syncthreads();
+    const uint32_t tok = static_cast<uint32_t>(tt[lane]);
+    const float s = tsc[lane];
+    float x[kCols];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) x[c] = 0.f;
+    const float* kr = kv + lane * pitch;
+    const float* q0 = qs + warp * kCols * a.d;
+    for (int k = 0; k < a.d; ++k) {
+      const float kvv = kr[k];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) x[c] = fmaf(q0[c * a.d + k], kvv, x[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      bool see = tok != 0xffffffffu;
+      if (see) {
+        const int t = static_cast<int>(tok & 0x7fffffffu);
+        const bool in_main = kv_sees(a, t, pos[c]);
+        see = (tok >> 31) ? !in_main : in_main;
+      }
+      x[c] = see ? x[c] * (xs * s) : -INFINITY;
+      float tm = x[c];
+      bool bad = see && !(s <= 3.4e38f);             // a block marked non-finite makes the result NaN
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+      const float mn = fmaxf(m[c], tm);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[c] - ref);             // 0 while nothing has been seen
+      float p = see ? exp2f(x[c] - ref) : 0.f;
+      if (bad) p = __int_as_float(0x7fc00000);
+      m[c] = mn;
+      float ps = p;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
+      l[c] = l[c] * f + ps;
+      const float pv = see ? p * s : 0.f;
+#pragma unroll
+      for (int k = 0; k < kMaxVpl; ++k) acc[c][k] *= f;
+      for (int t = 0; t < kTile; ++t) {
+        const float w = __shfl_sync(0xffffffffu, pv, t);
+        const float* vr = kv + t * pitch + a.voff + lane;
+#pragma unroll
+        for (int k = 0; k < kMaxVpl; ++k)
+          if (k < vpl && lane + 32 * k < a.dv) acc[c][k] = fmaf(w, vr[32 * k], acc[c][k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const int col = cb * kBlockCols + warp * kCols + c;
+    if (col >= ncol) continue;
+    if (a.splits > 1) {
+      const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + part) * ncol + col;
+#pragma unroll
+      for (int k = 0; k < kMaxVpl; ++k)
+        if (k < vpl && lane + 32 * k < a.dv) a.part_o[pc * a.dv + lane + 32 * k] = acc[c][k];
+      if (lane == 0) {
+        a.part_m[pc] = m[c];
+        a.part_l[pc] = l[c];
+      }
+    } else {
+      const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
+      const float r = l[c] == 0.f ? 0.f : 1.0f / l[c];
+#pragma unroll
+      for (int k = 0; k < kMaxVpl; ++k)
+        if (k < vpl && lane + 32 * k < a.dv) store_out(a.out, a.qdt, oc * a.dv + lane + 32 * k, acc[c][k] * r);
+      if (lane == 0 && a.lse != nullptr)
+        a.lse[oc] = l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.693147180559945f;
+    }
+  }
+}
+
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a column's parts.
+__global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendArgs a) {
+  pdl_wait();
+  const KvGeom& g = a.g;
+  const int hg = a.H / g.G, ncol = a.Tq * hg;
+  const long long u = blockIdx.x / ncol;
+  const int col = static_cast<int>(blockIdx.x % ncol);
+  const int head = static_cast<int>(u % g.G), b = static_cast<int>(u / g.G);
+  const size_t base = static_cast<size_t>(u) * a.splits * ncol + col;
+  float m = -INFINITY;
+  for (int p = 0; p < a.splits; ++p) m = fmaxf(m, a.part_m[base + static_cast<size_t>(p) * ncol]);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  for (int p = 0; p < a.splits; ++p) {
+    const size_t at = base + static_cast<size_t>(p) * ncol;
+    const float lp = a.part_l[at];
+    if (lp != 0.f) l += exp2f(a.part_m[at] - ref) * lp;
+  }
+  const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
+  const float r = l == 0.f ? 0.f : 1.0f / l;
+  for (int k = threadIdx.x; k < a.dv; k += blockDim.x) {
+    float o = 0.f;
+    for (int p = 0; p < a.splits; ++p) {
+      const size_t at = base + static_cast<size_t>(p) * ncol;
+      if (a.part_l[at] != 0.f) o = fmaf(exp2f(a.part_m[at] - ref), a.part_o[at * a.dv + k], o);
+    }
+    store_out(a.out, a.qdt, oc * a.dv + k, o * r);
+  }
+  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+}
+
+size_t simt_smem(const KvAttendArgs& a, int rows_used) {
+  const int pitch = rows_used | 1;
+  return static_cast<size_t>(kTile * pitch + kBlockCols * a.d + 2 * kTile + 2) * 4 + kTile * 8;
+}
+
+}  // namespace
+
+int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens) {
+  const long long units = static_cast<long long>(B) * G * ((ncol + kBlockCols - 1) / kBlockCols);
+  const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
+  // About four blocks per SM, at least two tiles in a part.
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({(4 * 148 + units - 1) / units, (tiles + 1) / 2, 256})));
+}
+
+int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s) {
+  const int ncol = a.Tq * (a.H / a.g.G), col_blocks = (ncol + kBlockCols - 1) / kBlockCols;
+  const int rows_used = (std::max(a.d, a.voff + a.dv) + 15) / 16 * 16;
+  const size_t smem = simt_smem(a, rows_used);
+  const cudaError_t e = cudaFuncSetAttribute(kv_attend_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
+  const long long grid = static_cast<long long>(a.g.B) * a.g.G * col_blocks * a.splits;
+  kv_attend_simt_kernel<<<static_cast<unsigned>(grid), kWarps * 32, smem, s>>>(a, col_blocks, rows_used);
+  return check_launch("kv_attend");
+}
+
+int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s) {
+  const long long grid = static_cast<long long>(a.g.B) * a.g.G * a.Tq * (a.H / a.g.G);
+  const cudaError_t e = launch_dependent(kv_attend_combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(128), 0, s, a);
+  if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
+  return check_launch("kv_attend_combine");
+}
+
+}  // namespace lsa
