@@ -47,16 +47,18 @@ int make_geom(const char* who, int B, int N, int G, int W, int block, int page, 
 }
 
 struct AttendWs {
+  bool tc;
   int splits;
   size_t o, m, l, total;
 };
 
-AttendWs attend_ws(int B, int Tq, int N, int H, int G, int dv, int sinks, int window, int cap) {
+AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int qdt, int sinks, int window, int cap) {
   AttendWs w{};
   const int ncol = Tq * (H / G);
   long long most = window < 0 ? N : std::min<long long>(N, static_cast<long long>(sinks) + window + Tq - 1);
   most += cap;
-  w.splits = kv_attend_splits_simt(std::max(B, 1), G, std::max(ncol, 1), most);
+  w.tc = kv_attend_tc_supported(N, d, dv, voff, qdt, std::max(ncol, 1));
+  w.splits = (w.tc ? kv_attend_splits_tc : kv_attend_splits_simt)(std::max(B, 1), G, std::max(ncol, 1), most);
   const size_t cols = static_cast<size_t>(B) * G * w.splits * ncol;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes, 256); return at; };
@@ -137,7 +139,7 @@ int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const i
 size_t lsa_kv_attend_workspace_bytes(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt,
                                      int sinks, int window, int cap) {
   if (attend_shape(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, cap) != LSA_OK) return 0;
-  return attend_ws(B, Tq, N, H, G, dv, sinks, window, cap).total + 256;
+  return attend_ws(B, Tq, N, H, G, d, dv, voff, qdt, sinks, window, cap).total + 256;
 }
 
 int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt, const void* q,
@@ -159,7 +161,7 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || !aligned(length, 4) ||
       (idx && (!aligned(idx, 4) || !aligned(count, 4))))
     return fail(LSA_ERR_INVALID_ARG, "kv_attend: misaligned pointer");
-  const AttendWs ws = attend_ws(B, Tq, N, H, G, dv, sinks, window, cap);
+  const AttendWs ws = attend_ws(B, Tq, N, H, G, d, dv, voff, qdt, sinks, window, cap);
   if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 256))
     return fail(LSA_ERR_NOMEM, "kv_attend: workspace %zu bytes (need %zu, 256-byte aligned)", workspace_bytes, ws.total);
   KvAttendArgs a{};
@@ -175,7 +177,7 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
   a.part_m = reinterpret_cast<float*>(base + ws.m);
   a.part_l = reinterpret_cast<float*>(base + ws.l);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = launch_kv_attend_simt(a, st);
+  rc = ws.tc ? launch_kv_attend_tc(a, st) : launch_kv_attend_simt(a, st);
   if (rc != LSA_OK || a.splits == 1) return rc;
   return launch_kv_attend_combine(a, st);
 }

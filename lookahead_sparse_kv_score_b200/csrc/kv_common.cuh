@@ -95,6 +95,9 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
   return e < 0 ? -1 : e;
 }
 
+bool kv_attend_tc_supported(int N, int d, int dv, int voff, int qdt, int ncol);
+int kv_attend_splits_tc(int B, int G, int ncol, long long max_tokens);
+int launch_kv_attend_tc(const KvAttendArgs& a, cudaStream_t s);
 int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens);
 int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s);
 int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s);
