@@ -48,7 +48,7 @@ int make_geom(const char* who, int B, int N, int G, int W, int block, int page, 
 
 struct AttendWs {
   bool tc;
-  int splits;
+  int cluster, splits;
   size_t o, m, l, total;
 };
 
@@ -56,9 +56,11 @@ AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, 
   AttendWs w{};
   const int ncol = Tq * (H / G);
   long long most = window < 0 ? N : std::min<long long>(N, static_cast<long long>(sinks) + window + Tq - 1);
-  most += cap;
-  w.tc = kv_attend_tc_supported(N, d, dv, voff, qdt, std::max(ncol, 1));
-  w.splits = (w.tc ? kv_attend_splits_tc : kv_attend_splits_simt)(std::max(B, 1), G, std::max(ncol, 1), most);
+  most += cap + 64;                            // and the numbering's empty places
+  w.tc = N <= (1 << 30) && kv_attend_tc_supported(most, d, dv, voff, qdt, std::max(ncol, 1));
+  w.cluster = 1;
+  if (w.tc) kv_attend_parts_tc(std::max(B, 1), G, std::max(ncol, 1), most, w.cluster, w.splits);
+  else w.splits = kv_attend_splits_simt(std::max(B, 1), G, std::max(ncol, 1), most);
   const size_t cols = static_cast<size_t>(B) * G * w.splits * ncol;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes, 256); return at; };
@@ -67,7 +69,7 @@ AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, 
     w.m = take(cols * 4);
     w.l = take(cols * 4);
   }
-  w.total = off;
+  w.total = std::max<size_t>(off, 256);
   return w;
 }
 
@@ -80,6 +82,8 @@ int attend_shape(int B, int Tq, int N, int H, int G, int d, int dv, int voff, in
   if (qdt != LSA_F32 && qdt != LSA_BF16) return fail(LSA_ERR_UNSUPPORTED, "kv_attend: query dtype %d", qdt);
   if (d > 576 || dv > 512 || voff + dv > 1024)
     return fail(LSA_ERR_UNSUPPORTED, "kv_attend: d = %d (at most 576), dv = %d (at most 512), voff + dv = %d (at most 1024)", d, dv, voff + dv);
+  if (static_cast<long long>(N) + cap > 0x7fff0000ll)
+    return fail(LSA_ERR_UNSUPPORTED, "kv_attend: N + cap = %lld (at most 2^31 - 2^16)", static_cast<long long>(N) + cap);
   if (static_cast<long long>(Tq) * (H / G) > 65536)
     return fail(LSA_ERR_UNSUPPORTED, "kv_attend: %lld query columns of a KV head (at most 65536)", static_cast<long long>(Tq) * (H / G));
   if (static_cast<long long>(B) * Tq * H > (1ll << 24))
@@ -139,7 +143,7 @@ int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const i
 size_t lsa_kv_attend_workspace_bytes(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt,
                                      int sinks, int window, int cap) {
   if (attend_shape(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, cap) != LSA_OK) return 0;
-  return attend_ws(B, Tq, N, H, G, d, dv, voff, qdt, sinks, window, cap).total + 256;
+  return attend_ws(B, Tq, N, H, G, d, dv, voff, qdt, sinks, window, cap).total;
 }
 
 int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt, const void* q,
@@ -177,7 +181,7 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
   a.part_m = reinterpret_cast<float*>(base + ws.m);
   a.part_l = reinterpret_cast<float*>(base + ws.l);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = ws.tc ? launch_kv_attend_tc(a, st) : launch_kv_attend_simt(a, st);
+  rc = ws.tc ? launch_kv_attend_tc(a, ws.cluster, st) : launch_kv_attend_simt(a, st);
   if (rc != LSA_OK || a.splits == 1) return rc;
   return launch_kv_attend_combine(a, st);
 }

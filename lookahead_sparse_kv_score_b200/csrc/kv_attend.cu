@@ -176,8 +176,11 @@ kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
   }
 }
 
-// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a column's parts.
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a column's parts: a block a column,
+// the parts' weights first (a thread a part), then four columns a thread.
 __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendArgs a) {
+  __shared__ float wt[256];
+  __shared__ float red[8];
   pdl_wait();
   const KvGeom& g = a.g;
   const int hg = a.H / g.G, ncol = a.Tq * hg;
@@ -185,24 +188,61 @@ __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendAr
   const int col = static_cast<int>(blockIdx.x % ncol);
   const int head = static_cast<int>(u % g.G), b = static_cast<int>(u / g.G);
   const size_t base = static_cast<size_t>(u) * a.splits * ncol + col;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float pm[2], pl[2];
   float m = -INFINITY;
-  for (int p = 0; p < a.splits; ++p) m = fmaxf(m, a.part_m[base + static_cast<size_t>(p) * ncol]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  for (int p = 0; p < a.splits; ++p) {
-    const size_t at = base + static_cast<size_t>(p) * ncol;
-    const float lp = a.part_l[at];
-    if (lp != 0.f) l += exp2f(a.part_m[at] - ref) * lp;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int p = threadIdx.x + 128 * k;
+    pl[k] = p < a.splits ? a.part_l[base + static_cast<size_t>(p) * ncol] : 0.f;
+    pm[k] = p < a.splits ? a.part_m[base + static_cast<size_t>(p) * ncol] : 0.f;
+    if (pl[k] != 0.f) m = fmaxf(m, pm[k]);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float l = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float w = pl[k] != 0.f ? exp2f(pm[k] - m) : 0.f;
+    if (threadIdx.x + 128 * k < 256) wt[threadIdx.x + 128 * k] = w;
+    l += pl[k] != 0.f ? w * pl[k] : 0.f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) red[4 + warp] = l;
+  __syncthreads();
+  l = (red[4] + red[5]) + (red[6] + red[7]);
   const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
   const float r = l == 0.f ? 0.f : 1.0f / l;
-  for (int k = threadIdx.x; k < a.dv; k += blockDim.x) {
-    float o = 0.f;
-    for (int p = 0; p < a.splits; ++p) {
-      const size_t at = base + static_cast<size_t>(p) * ncol;
-      if (a.part_l[at] != 0.f) o = fmaf(exp2f(a.part_m[at] - ref), a.part_o[at * a.dv + k], o);
+  const float* po = a.part_o + base * a.dv;
+  const size_t step = static_cast<size_t>(ncol) * a.dv;
+  if (a.dv % 4 == 0) {
+    for (int k = threadIdx.x; k < a.dv / 4; k += 128) {
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+      for (int p = 0; p < a.splits; ++p) {
+        const float4 v = *reinterpret_cast<const float4*>(po + p * step + 4 * k);
+        const float w = wt[p];
+        if (w != 0.f) {                                    // a part without tokens has stored nothing
+          o[0] = fmaf(w, v.x, o[0]);
+          o[1] = fmaf(w, v.y, o[1]);
+          o[2] = fmaf(w, v.z, o[2]);
+          o[3] = fmaf(w, v.w, o[3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) store_out(a.out, a.qdt, oc * a.dv + 4 * k + e, o[e] * r);
     }
-    store_out(a.out, a.qdt, oc * a.dv + k, o * r);
+  } else {
+    for (int k = threadIdx.x; k < a.dv; k += 128) {
+      float o = 0.f;
+      for (int p = 0; p < a.splits; ++p)
+        if (wt[p] != 0.f) o = fmaf(wt[p], po[p * step + k], o);
+      store_out(a.out, a.qdt, oc * a.dv + k, o * r);
+    }
   }
   if (threadIdx.x == 0 && a.lse != nullptr) a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
 }

@@ -17,7 +17,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHold = 8;        // 8-element vectors a thread keeps in registers between the passes
-constexpr uint32_t kScaleMinBits = (127u - 24u) << 23;
 constexpr uint32_t kNanBits = 0x7fc00000u;
 
 // Eight consecutive elements as fp32 bits.

@@ -53,28 +53,30 @@ struct KvAttendArgs {
 };
 
 // The tokens one sequence's queries can see, in one numbering v = 0 .. total-1: the first
-// tokens, the window (of all queries together) and the listed entries.
+// tokens, the window (of all queries together) and the listed entries.  The window starts on a
+// multiple of 16 tokens, and the first tokens are padded to 32 places, so that runs of a
+// page's rows stay runs of places; the places without a token are empty.
 struct KvSpan {
-  int len, first, lo, n_main, total;
+  int len, first, pad, lo, start, n_main, total;
 };
 
 __device__ __forceinline__ KvSpan kv_span(const KvAttendArgs& a, int b) {
   KvSpan s;
   s.len = min(max(__ldg(a.length + b), 0), a.g.N);
-  if (a.window < 0) {
-    s.first = 0;
-    s.lo = 0;
-    s.n_main = s.len;
-  } else {
+  const int listed = a.idx != nullptr ? max(0, min(__ldg(a.count + b), a.cap)) : 0;
+  s.first = s.pad = s.lo = s.start = 0;
+  s.n_main = s.len;
+  if (a.window >= 0) {
     s.first = min(a.sinks, s.len);
     // lowest position in any query's window; len - Tq is the first query's position
     const long long lo = static_cast<long long>(s.len) - a.Tq - a.window + 1;
     s.lo = static_cast<int>(lo > s.first ? lo : s.first);
-    s.n_main = s.first + (a.window > 0 && s.len > s.lo ? s.len - s.lo : 0);
+    s.start = max(s.first, s.lo & ~15);
+    const bool window = a.window > 0 && s.len > s.lo;
+    s.pad = window && s.first > 0 && s.first <= 0x7fffffff - 31 ? (s.first + 31) & ~31 : s.first;
+    s.n_main = s.pad + (window ? s.len - s.start : 0);
   }
-  int n = s.n_main;
-  if (a.idx != nullptr) n += max(0, min(__ldg(a.count + b), a.cap));
-  s.total = n;
+  s.total = s.n_main + listed;
   return s;
 }
 
@@ -83,10 +85,15 @@ __device__ __forceinline__ bool kv_sees(const KvAttendArgs& a, int t, int p) {
   return t <= p && (a.window < 0 || t < a.sinks || t > p - static_cast<long long>(a.window));
 }
 
-// Token v of the numbering, or -1 for a list entry that is padding or out of range.
+// Token v of the numbering, or -1 for an empty place and for a list entry that is padding or
+// out of range.
 __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, int b, int v, bool& main) {
   main = v < s.n_main;
-  if (main) return v < s.first ? v : s.lo + (v - s.first);
+  if (main) {
+    if (v < s.pad) return v < s.first ? v : -1;
+    const int t = s.start + (v - s.pad);
+    return t < s.lo ? -1 : t;
+  }
   const int e = __ldg(a.idx + static_cast<size_t>(b) * a.cap + (v - s.n_main));
   if (e >= s.len) {
     raise_status(a.status, LSA_ERR_RANGE);
@@ -95,9 +102,10 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
   return e < 0 ? -1 : e;
 }
 
-bool kv_attend_tc_supported(int N, int d, int dv, int voff, int qdt, int ncol);
-int kv_attend_splits_tc(int B, int G, int ncol, long long max_tokens);
-int launch_kv_attend_tc(const KvAttendArgs& a, cudaStream_t s);
+bool kv_attend_tc_supported(long long max_tokens, int d, int dv, int voff, int qdt, int ncol);
+// Blocks of a cluster and clusters of a unit (KvAttendArgs::splits) for the tensor-core path.
+void kv_attend_parts_tc(int B, int G, int ncol, long long max_tokens, int& cluster, int& groups);
+int launch_kv_attend_tc(const KvAttendArgs& a, int cluster, cudaStream_t s);
 int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens);
 int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s);
 int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s);
