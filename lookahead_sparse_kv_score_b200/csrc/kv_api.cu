@@ -59,7 +59,7 @@ AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, 
   most += cap + 64;                            // and the numbering's empty places
   w.tc = N <= (1 << 30) && kv_attend_tc_supported(most, d, dv, voff, qdt, std::max(ncol, 1));
   w.cluster = 1;
-  if (w.tc) kv_attend_parts_tc(std::max(B, 1), G, std::max(ncol, 1), most, w.cluster, w.splits);
+  if (w.tc) kv_attend_parts_tc(std::max(B, 1), G, std::max(ncol, 1), d, dv, voff, most, w.cluster, w.splits);
   else w.splits = kv_attend_splits_simt(std::max(B, 1), G, std::max(ncol, 1), most);
   const size_t cols = static_cast<size_t>(B) * G * w.splits * ncol;
   size_t off = 0;

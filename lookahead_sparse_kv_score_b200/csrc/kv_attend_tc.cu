@@ -45,6 +45,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -65,8 +66,8 @@ struct Shape {
   static constexpr int kGroups = C == 16 ? 1 : 2;
   static constexpr int NC = C / kGroups;                   // columns of a weights warp
   static constexpr int kWeights = 4 * kGroups;             // warps
-  static constexpr int kMmaWarp = 4 + kWeights;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kMmaWarp = 4 + kWeights;            // the first of two: scores, values
+  static constexpr int kThreads = 32 * (kMmaWarp + 2);
   static constexpr int kBlocks = C == 64 ? 1 : 2;          // blocks an SM, where shared memory allows
   static constexpr uint32_t kTmemCols = C == 64 ? 512 : C == 32 ? 256 : 128;
 };
@@ -133,25 +134,15 @@ Plan make_plan(int d, int dv, int voff, int C, int limit) {
 struct AttendTc {
   KvAttendArgs a;
   Plan p;
-  int col_groups, cluster;
+  int col_groups, cluster, hg;
   int run;          // rows of a TMA box (16 or 32 places whose rows follow one another), 0: no maps
 };
 
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr) {     // 128-byte swizzle, 1024-byte groups
-  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-__device__ __forceinline__ uint64_t desc64(uint32_t saddr) {      // 64-byte swizzle, 512-byte groups
-  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>(512u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(4u) << 61;
-  return d;
+// Shared-memory matrix descriptors: start address and version word; groups of eight rows (a
+// row is 128 or 64 bytes, as wide as the swizzle) `group` bytes apart; swizzle 2 (128 bytes) or 4 (64).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t group, uint32_t swizzle) {
+  return (group >> 4) | (1u << 14) | (swizzle << 29);
 }
 
 // kind::f8f6f4, fp32 accumulators, M = 128: operand types (0 e4m3, 1 e5m2), both operands
@@ -238,9 +229,38 @@ __device__ __forceinline__ float warp_max(float x) {               // NaN is ign
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrives at the barrier when this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Whether the barrier's phase has completed, without waiting (try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+// The MMA warp runs converged and an elected lane issues.  A descriptor's low word is made
+// uniform once a chunk, so that the ones behind it are sums in uniform registers: an MMA then
+// takes its 48 clocks (N = 64; 64 with N = 128, shared memory's rate), where descriptors in
+// vector registers made it 97.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(r)::"memory");
+  return r != 0;
+}
+__device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t id,
+                                       uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem), "r"(a_lo), "r"(a_hi),
+               "r"(b_lo), "r"(b_hi), "r"(id), "r"(acc) : "memory");
 }
 
 // Adds to the bytes a barrier's phase waits for, without arriving.
@@ -318,23 +338,29 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
   uint64_t* pfull = bars + 38;
   uint64_t* pdone = bars + 39;
   uint64_t* qfull = bars + 40;
-  uint64_t* drain = bars + 41;
+  uint64_t* drain = bars + 41;              // both MMA warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 42);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 43);
+  uint64_t* sempty = bars + 44;             // [2]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hg = a.H / g.G, ncol = a.Tq * hg;
-  int u = blockIdx.x;
-  const int rank = u % t.cluster; u /= t.cluster;
-  const int cg = u % t.col_groups; u /= t.col_groups;
-  const int grp = u % a.splits; u /= a.splits;             // a.splits: clusters of a unit
-  const int head = u % g.G, b = u / g.G;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int hg = t.hg, ncol = a.Tq * hg;
+  // (a division only where there is something to divide)
+  uint32_t u = blockIdx.x;
+  auto digit = [&](int count) -> int {
+    if (count == 1) return 0;
+    const uint32_t q = u / count, r = u - q * count;
+    u = q;
+    return static_cast<int>(r);
+  };
+  const int rank = digit(t.cluster), cg = digit(t.col_groups), grp = digit(a.splits), head = digit(g.G);   // a.splits: clusters of a unit
+  const int b = static_cast<int>(u);
   const int c_base = cg * C, n_c = min(C, ncol - c_base);
   const KvSpan sp = kv_span(a, b);
   const int tiles = (sp.total + kTile - 1) / kTile;
   const int parts = a.splits * t.cluster, part = grp * t.cluster + rank;
-  const int tile0 = static_cast<int>(static_cast<long long>(tiles) * part / parts);
-  const int n = static_cast<int>(static_cast<long long>(tiles) * (part + 1) / parts) - tile0;
+  const int each = parts == 1 ? tiles : tiles / parts, more = tiles - each * parts;   // the first `more` parts have one tile more
+  const int tile0 = part * each + min(part, more), n = each + (part < more ? 1 : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < pl.stages * pl.n_full; ++s) {
@@ -351,7 +377,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     mbar_init(pfull, Sh::kWeights);
     mbar_init(pdone, 1);
     mbar_init(qfull, Sh::kWeights);
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
+    mbar_init(&sempty[0], Sh::kWeights);
+    mbar_init(&sempty[1], Sh::kWeights);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -367,6 +395,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     const int n_kf = pl.n_k - pl.tail, gap = max(pl.v0 - n_kf, 0);   // chunks between keys and values are not read
     const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
     const uint64_t policy = normal_policy();
+    const int piece = lane & 7, r_in = lane >> 3;          // a lane's 16 bytes of a chunk and its row of four
+    const uint8_t* lane_base = g.rows + static_cast<size_t>(head) * g.W + piece * 16;
     // A token takes three dependent loads (list, table, scale beside the row): each is issued
     // a tile ahead of the next.  tok: the tile behind the next; page, scale: the next tile.
     auto load_token = [&](int j, bool& main) -> int {
@@ -422,11 +452,16 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       // whether the warp's rows are runs of t.run rows, for the TMA
       const int in_run = t.run > 0 ? lane & (t.run - 1) : 0, run_first = __shfl_sync(0xffffffffu, row, lane - in_run);
       const bool runs = __all_sync(0xffffffffu, t.run > 0 && row >= 0 && row == run_first + in_run);
-      uint32_t from[8], from_t[4];                         // this lane's rows of the copies, four and eight rows an instruction
+      // This lane's rows of the copies, four rows an instruction, and whether all are there.
+      const uint8_t* src[8];
+      uint32_t there = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) from[k] = static_cast<uint32_t>(__shfl_sync(0xffffffffu, row, k * 4 + (lane >> 3)));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) from_t[k] = static_cast<uint32_t>(__shfl_sync(0xffffffffu, row, k * 8 + (lane >> 2)));
+      for (int k = 0; k < 8; ++k) {
+        const int r = __shfl_sync(0xffffffffu, row, k * 4 + (lane >> 3));
+        there |= (r >= 0 ? 1u : 0u) << k;
+        src[k] = lane_base + static_cast<size_t>(max(r, 0)) * row_bytes;
+      }
+      const bool whole = __all_sync(0xffffffffu, there == 0xffu);
       const int row0 = __shfl_sync(0xffffffffu, row, 0), row16 = __shfl_sync(0xffffffffu, row, 16);
       for (int c = 0; c <= pl.n_full && ok; ++c) {         // c = n_full: the tail
         if (c == pl.n_full && !pl.tail) break;
@@ -451,25 +486,28 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
           __syncwarp();
           mbar_arrive(full_bar);
         } else if (!is_tail) {
-          const int piece = lane & 7, r_in = lane >> 3;
           const bool in = col + piece * 16 < g.W;          // past the row's end there is nothing to read
-          const uint8_t* base = g.rows + static_cast<size_t>(head) * g.W + (in ? col + piece * 16 : 0);
-          const uint32_t at = smem_u32(to) + r_in * 128;
+          const uint32_t at0 = smem_u32(to) + r_in * 128 + ((piece ^ r_in) * 16), at1 = at0 ^ 64;
+          if (whole && col + 128 <= g.W) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const bool real = static_cast<int>(from[k]) >= 0;
-            copy16(at + k * 512 + ((piece ^ (((k & 1) << 2) + r_in)) * 16), base + (real ? from[k] * row_bytes : 0), real && in ? 16u : 0u);
+            for (int k = 0; k < 8; ++k) copy16(((k & 1) ? at1 : at0) + k * 512, src[k] + col);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const bool real = in && ((there >> k) & 1);
+              copy16(((k & 1) ? at1 : at0) + k * 512, src[k] + (in ? col : 0), real ? 16u : 0u);
+            }
           }
           copies_arrive(full_bar);
         } else {
-          const int piece = lane & 3, r_in = lane >> 2;
-          const bool in = col + piece * 16 < g.W;
-          const uint8_t* base = g.rows + static_cast<size_t>(head) * g.W + (in ? col + piece * 16 : 0);
-          const uint32_t at = smem_u32(to) + r_in * 64 + ((piece ^ ((r_in >> 1) & 3)) * 16);
+          const int p4 = lane & 3, r8 = lane >> 2;         // eight rows an instruction
+          const bool in = col + p4 * 16 < g.W;
+          const uint8_t* base = g.rows + static_cast<size_t>(head) * g.W + (in ? col + p4 * 16 : 0);
+          const uint32_t at = smem_u32(to) + r8 * 64 + ((p4 ^ ((r8 >> 1) & 3)) * 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const bool real = static_cast<int>(from_t[k]) >= 0;
-            copy16(at + k * 512, base + (real ? from_t[k] * row_bytes : 0), real && in ? 16u : 0u);
+            const int r = __shfl_sync(0xffffffffu, row, k * 8 + r8);
+            copy16(at + k * 512, base + static_cast<size_t>(max(r, 0)) * row_bytes, r >= 0 && in ? 16u : 0u);
           }
           copies_arrive(full_bar);
         }
@@ -486,90 +524,89 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     // every copy has landed before the block goes on: on the way out of an abort too
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok) drain_boxes();
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t ring_u = smem_u32(ring), q_u = smem_u32(qimg), p_u = smem_u32(pbuf), tail_u = smem_u32(tails);
-      const int n_kf = pl.n_k - pl.tail, n_f = pl.n_full, n_v = pl.n_v;
-      const int v_slot0 = plan_v_slot(pl, pl.v0);          // value chunks lie in consecutive slots from here
-      constexpr uint32_t id_s = idesc(2 * C, 0, 0), id_hi = idesc(C, 0, 1), id_lo = idesc(C, 1, 1);
-      const uint64_t ring_d = desc128(ring_u), q_d = desc128(q_u), p_d = desc128(p_u), tail_d = desc64(tail_u),
-                     qt_d = desc64(q_u + n_kf * (2 * C * 128));
-      bool ok = n == 0 || mbar_wait(qfull, 0, abort_flag);
-      // Steps of one chunk, whichever is ready: the scores of tile js (at most one tile ahead of
-      // the values, for two S buffers), or the values of tile jv once its weights are there.
-      int js = 0, cs = 0, ss = 0, tss = 0, jv = 0, cv = 0, sv = 0;   // tile, chunk, stage (and tail)
-      uint32_t ph = 0, tph = 0, phv = 0;
-      const int s_steps = n_kf + pl.tail;
-      uint32_t idle = 0;
-      unsigned long long t0 = 0;
-      while (ok && jv < n) {
-        bool moved = false;
-        if (js < n && js <= jv + 1) {
-          const uint32_t d_t = tmem + (js & 1) * (2 * C);
-          const uint32_t acc = cs > 0 ? 1u : 0u;
-          if (cs < n_kf) {
-            const int slot = ss * n_f + cs;
-            if (mbar_try_wait(&full[slot], ph)) {
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, to the MMAs
-              tc_fence_after();
-              const uint64_t ad = ring_d + slot * (kChunkBytes >> 4), bd = q_d + cs * ((2 * C * 128) >> 4);
-              const int left = pl.ksteps - 4 * cs;
-              mma<true>(d_t, ad, bd, id_s, acc);
-              if (left > 1) mma<true>(d_t, ad + 2, bd + 2, id_s, 1u);
-              if (left > 2) mma<true>(d_t, ad + 4, bd + 4, id_s, 1u);
-              if (left > 3) mma<true>(d_t, ad + 6, bd + 6, id_s, 1u);
-              if (cs < v_slot0 || cs >= v_slot0 + n_v) mma_commit(&empty[slot]);   // keys alone
-              moved = true;
-            }
-          } else if (mbar_try_wait(&tfull[tss], tph)) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_after();
-            mma<true>(d_t, tail_d + tss * (kTailBytes >> 4), qt_d, id_s, acc);
-            if (pl.ksteps - 4 * n_kf > 1) mma<true>(d_t, tail_d + tss * (kTailBytes >> 4) + 2, qt_d + 2, id_s, 1u);
-            mma_commit(&tempty[tss]);
-            if (++tss == pl.tstages) { tss = 0; tph ^= 1; }
-            moved = true;
+  } else if (warp >= kMmaWarp) {
+    // ---------------------------------------------------------------- MMA issuers
+    // One warp for the scores and one for the values: an issue waits while the tensor core is
+    // busy, and a barrier test or a commit (100 to 150 clocks) in between would leave it idle.
+    const int n_kf = pl.n_k - pl.tail, n_f = pl.n_full, n_v = pl.n_v, n_sc = n_kf + pl.tail;
+    const int v_slot0 = plan_v_slot(pl, pl.v0);            // value chunks lie in consecutive slots from here
+    constexpr uint32_t id_s = idesc(2 * C, 0, 0), id_hi = idesc(C, 0, 1), id_lo = idesc(C, 1, 1);
+    constexpr uint32_t kHi128 = desc_hi(1024, 2), kHi64 = desc_hi(512, 4);
+    const uint32_t ring_lo = desc_lo(smem_u32(ring));
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)); };
+    bool ok = true;
+    if (warp == kMmaWarp) {
+      const uint32_t q_lo = desc_lo(smem_u32(qimg)), tail_lo = desc_lo(smem_u32(tails)), qt_lo = desc_lo(smem_u32(qimg) + n_kf * (2 * C * 128));
+      int s = 0, ts = 0;
+      uint32_t ph = 0, tph = 0;
+      if (n > 0) ok = wait(qfull, 0);
+      for (int j = 0; ok && j < n; ++j) {
+        ok = wait(&sempty[j & 1], ((j >> 1) & 1) ^ 1);
+        const uint32_t d_t = uniform(tmem + (j & 1) * (2 * C));
+        for (int c = 0; ok && c < n_kf; ++c) {
+          const int slot = s * n_f + c;
+          if (!(ok = wait(&full[slot], ph))) break;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, to the MMAs
+          tc_fence_after();
+          const int left = pl.ksteps - 4 * c;
+          const uint32_t ad = uniform(ring_lo + slot * (kChunkBytes >> 4)), bd = uniform(q_lo + c * ((2 * C * 128) >> 4));
+          if (elect()) {
+            mma_lo(d_t, ad, kHi128, bd, kHi128, id_s, c > 0 ? 1u : 0u);
+            if (left > 1) mma_lo(d_t, ad + 2, kHi128, bd + 2, kHi128, id_s, 1u);
+            if (left > 2) mma_lo(d_t, ad + 4, kHi128, bd + 4, kHi128, id_s, 1u);
+            if (left > 3) mma_lo(d_t, ad + 6, kHi128, bd + 6, kHi128, id_s, 1u);
+            if (c < v_slot0 || c >= v_slot0 + n_v) mma_commit(&empty[slot]);   // keys alone
+            if (c + 1 == n_sc) mma_commit(&sfull[j & 1]);
           }
-          if (moved && ++cs == s_steps) {
-            mma_commit(&sfull[js & 1]);
-            ++js;
-            cs = 0;
-            if (++ss == pl.stages) { ss = 0; ph ^= 1; }
-          }
+          __syncwarp();
         }
-        if (!moved && jv < js) {
-          const int c = v_slot0 + cv, slot = sv * n_f + c;
-          if ((cv > 0 || mbar_try_wait(pfull, jv & 1)) && (c < n_kf || mbar_try_wait(&full[slot], phv))) {
-            if (c >= n_kf) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            tc_fence_after();
-            const uint64_t ad = ring_d + slot * (kChunkBytes >> 4);
-            const uint32_t d_t = tmem + kO + cv * C;
+        if (ok && pl.tail && (ok = wait(&tfull[ts], tph))) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc_fence_after();
+          const uint32_t ad = uniform(tail_lo + ts * (kTailBytes >> 4)), bd = uniform(qt_lo);
+          if (elect()) {
+            mma_lo(d_t, ad, kHi64, bd, kHi64, id_s, n_kf > 0 ? 1u : 0u);
+            if (pl.ksteps - 4 * n_kf > 1) mma_lo(d_t, ad + 2, kHi64, bd + 2, kHi64, id_s, 1u);
+            mma_commit(&sfull[j & 1]);
+            mma_commit(&tempty[ts]);
+          }
+          __syncwarp();
+        }
+        if (++s == pl.stages) { s = 0; ph ^= 1; }
+        if (++ts == pl.tstages) { ts = 0; tph ^= 1; }
+      }
+    } else {
+      const uint32_t bd = uniform(desc_lo(smem_u32(pbuf)));
+      int s = 0;
+      uint32_t ph = 0;
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = wait(pfull, j & 1))) break;
+        const uint32_t acc = j > 0 ? 1u : 0u;
+        for (int m = 0; m < n_v; ++m) {
+          const int c = v_slot0 + m, slot = s * n_f + c;
+          if (c >= n_kf) {                                 // a chunk without keys: nobody has waited for it yet
+            if (!(ok = wait(&full[slot], ph))) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          tc_fence_after();
+          const uint32_t ad = uniform(ring_lo + slot * (kChunkBytes >> 4)), d_t = uniform(tmem + kO + m * C);
+          if (elect()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              mma<true>(d_t, ad + ks * 256, p_d + ks * 256, id_hi, jv > 0 || ks > 0 ? 1u : 0u);
-              mma<true>(d_t, ad + ks * 256, p_d + ks * 256 + 4, id_lo, 1u);
+              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 256, kHi128, id_hi, ks > 0 ? 1u : acc);
+              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 256 + 4, kHi128, id_lo, 1u);
             }
             mma_commit(&empty[slot]);
-            moved = true;
-            if (++cv == n_v) {
-              mma_commit(pdone);
-              cv = 0;
-              ++jv;
-              if (++sv == pl.stages) { sv = 0; phv ^= 1; }
-            }
+            if (m + 1 == n_v) mma_commit(pdone);
           }
+          __syncwarp();
         }
-        if (moved) {
-          idle = 0;
-        } else if ((++idle & 63u) == 0) {                  // bounded like every wait
-          if (idle == 64) t0 = global_timer();
-          if (*abort_flag || global_timer() - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            ok = false;
-          }
-        }
+        if (++s == pl.stages) { s = 0; ph ^= 1; }
       }
+    }
+    // every MMA this warp issued is done before the tensor memory is given up (commits count the
+    // elected lane's: it issued them all)
+    if (elect()) {
       mma_commit(drain);
       volatile int no_abort = 0;
       mbar_wait(drain, 0, &no_abort);
@@ -591,7 +628,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         uint4 v[kBatch][3];                                // d <= 576: at most 72 groups of 8
 #pragma unroll
         for (int k2 = 0; k2 < kBatch; ++k2) {
-          const int c = (cb + k2) * Sh::kWeights + warp - 4, col = c_base + c, i = col / hg;
+          const int c = (cb + k2) * Sh::kWeights + warp - 4, col = c_base + c, i = a.Tq == 1 ? 0 : col / hg;
           const __nv_bfloat16* qrow = q + ((static_cast<size_t>(b) * a.Tq + i) * a.H + head * hg + (col - i * hg)) * a.d;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
@@ -599,9 +636,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
             v[k2][k] = c < n_c && e < a.d ? __ldg(reinterpret_cast<const uint4*>(qrow + e)) : make_uint4(0, 0, 0, 0);
           }
         }
+        float inv[kBatch];
 #pragma unroll
         for (int k2 = 0; k2 < kBatch; ++k2) {
-          const int c = (cb + k2) * Sh::kWeights + warp - 4;
           uint32_t m = 0;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
@@ -613,34 +650,39 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
           const bool finite = m < 0x7f800000u;
           // s = 2^e, the smallest (from 2^-100) with max|q| / s <= 448
           const int se = max(static_cast<int>(m >> 23) - 8 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0), 27);
-          const float inv = finite ? __uint_as_float(static_cast<uint32_t>(254 - se) << 23) : 0.f;
+          inv[k2] = finite ? __uint_as_float(static_cast<uint32_t>(254 - se) << 23) : 0.f;
           if (lane == 0) {
+            const int c = (cb + k2) * Sh::kWeights + warp - 4;
             const float sc = finite ? __uint_as_float(static_cast<uint32_t>(se) << 23) : __uint_as_float(0x7fc00000u);
             qf[c] = c < n_c ? sc * a.sm * 1.44269504088896f : 0.f;
             nref[c] = kUnset;
-            qi[c] = static_cast<uint16_t>(min(c_base + c, ncol - 1) / hg);
+            qi[c] = static_cast<uint16_t>(a.Tq == 1 ? 0 : min(c_base + c, ncol - 1) / hg);
           }
+        }
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int e = (lane + 32 * k) * 8;
-            if (e >= dpad) continue;
+        for (int k = 0; k < 3; ++k) {
+          const int e = (lane + 32 * k) * 8;
+          if (e >= dpad) continue;
+          const int chunk = e >> 7, j = (e & 127) >> 4;
+          const bool main_chunk = chunk < n_kf;
+          uint8_t* at = qimg + (main_chunk ? chunk : n_kf) * (2 * C * 128) + (e & 8);
+          const int second = C * (main_chunk ? 128 : 64);  // C is a multiple of 8: one swizzle for both rows
+#pragma unroll
+          for (int k2 = 0; k2 < kBatch; ++k2) {
+            const int c = (cb + k2) * Sh::kWeights + warp - 4;
             const uint32_t w[4] = {v[k2][k].x, v[k2][k].y, v[k2][k].z, v[k2][k].w};
+            const float2 inv2 = make_float2(inv[k2], inv[k2]);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float f0 = __uint_as_float(w[x] << 16) * inv, f1 = __uint_as_float(w[x] & 0xffff0000u) * inv;
-              hi[x] = __nv_cvt_float2_to_fp8x2(make_float2(f0, f1), __NV_SATFINITE, __NV_E4M3);
+              const float2 f = mul2(pair(w[x] << 16, w[x] & 0xffff0000u), inv2);
+              hi[x] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
               const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[x]), __NV_E4M3)));
-              lo[x] = __nv_cvt_float2_to_fp8x2(make_float2(f0 - h.x, f1 - h.y), __NV_SATFINITE, __NV_E4M3);
+              lo[x] = __nv_cvt_float2_to_fp8x2(make_float2(f.x - h.x, f.y - h.y), __NV_SATFINITE, __NV_E4M3);
             }
-            const uint2 hv = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            const uint2 lv = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            const int chunk = e / 128, j = (e % 128) / 16, x = e % 16;   // C is a multiple of 8: one swizzle for both rows
-            const bool main_chunk = chunk < n_kf;
-            uint8_t* base = qimg + (main_chunk ? chunk : n_kf) * (2 * C * 128) +
-                            (main_chunk ? c * 128 + ((j ^ (c & 7)) * 16) : c * 64 + ((j ^ ((c >> 1) & 3)) * 16)) + x;
-            *reinterpret_cast<uint2*>(base) = hv;
-            *reinterpret_cast<uint2*>(base + C * (main_chunk ? 128 : 64)) = lv;
+            uint8_t* base = at + (main_chunk ? c * 128 + ((j ^ (c & 7)) * 16) : c * 64 + ((j ^ ((c >> 1) & 3)) * 16));
+            *reinterpret_cast<uint2*>(base) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(base + second) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
           }
         }
       }
@@ -760,6 +802,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         group_sync(bar_id);                                // the new reference, to all
       }
       if (stop) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sempty[j & 1]);
       // Of a NaN scale only the columns that see the token become NaN.
       const float inv = scale > 0.f ? 1.0f / scale : 1.0f;
       uint32_t hw[NC / 4], lw[NC / 4];
@@ -793,15 +838,23 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     // [C][128 n_v] fp32 (every tile has been read).
     if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
     tc_fence_after();
-    float mine = 0.f;
+    // Each step halves the columns a lane holds; lane l ends with column l (NC = 16: l / 2).
+    float v[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float v = c & 1 ? l[c / 2].y : l[c / 2].x;
+    for (int c = 0; c < NC; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
+    int o = 16;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == c) mine = v;
+    for (int w = NC / 2; w >= 1; w /= 2) {
+#pragma unroll
+      for (int c = 0; c < w; ++c) {
+        const bool up = (lane & o) != 0;
+        const float keep = up ? v[c + w] : v[c], give = up ? v[c] : v[c + w];
+        v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+      o >>= 1;
     }
-    if (lane < NC) *scratch(quad * 32 + lane) = mine;
+    if constexpr (NC == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+    *scratch(quad * 32 + (NC == 16 ? lane >> 1 : lane)) = v[0];
     group_sync(bar_id);
     if (quad == 0 && lane < NC)
       qf[c0 + lane] = (*scratch(lane) + *scratch(32 + lane)) + (*scratch(64 + lane) + *scratch(96 + lane));
@@ -818,7 +871,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
       float* to = os + m * 128 + c0 * pitch;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) to[c * pitch] = __uint_as_float(o[c]);
+      for (int c = 0; c < NC; ++c) {
+        *to = __uint_as_float(o[c]);
+        to += pitch;
+      }
     }
   }
   tc_fence_before();
@@ -833,11 +889,13 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
   // This block's share of the columns: out = sum_x w_x O_x, w_x = 2^(r_x - r) (over the sum of
   // the weights when the unit has one cluster).
   {
-    const int X = t.cluster, share = C / X, cs = rank * share;
+    const int X = t.cluster, share = C >> (31 - __clz(X)), cs = rank * share;
     float* wtab = reinterpret_cast<float*>(pbuf);          // [X][share]: weights
     float2* rl = reinterpret_cast<float2*>(pbuf + C * 4);  // [X][share]: reference, sum
+    int* place = reinterpret_cast<int*>(pbuf + C * 12);    // [share]: output row (or part row) of a column
+    const int xl = 31 - __clz(X), sl = 31 - __clz(share);  // both are powers of two
     if (threadIdx.x < C) {
-      const int x = threadIdx.x / share, c = cs + threadIdx.x - x * share;
+      const int x = threadIdx.x >> sl, c = cs + (threadIdx.x & (share - 1));
       rl[threadIdx.x] = make_float2(-peer_ld(peer(smem_u32(nref + c), x)), peer_ld(peer(smem_u32(qf + c), x)));
     }
     __syncthreads();
@@ -857,12 +915,13 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         const float2 v = rl[x * share + threadIdx.x];
         wtab[x * share + threadIdx.x] = v.y != 0.f ? ex2(v.x - m) * r : 0.f;
       }
-      if (c < n_c) {
-        if (a.splits == 1) {
-          const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
-          if (a.lse) a.lse[oc] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
-        } else {
-          const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
+      if (a.splits == 1) {
+        const int i = a.Tq == 1 ? 0 : col / hg, oc = (b * a.Tq + i) * a.H + head * hg + col - i * hg;   // at most 2^24
+        place[threadIdx.x] = oc;
+        if (a.lse && c < n_c) a.lse[oc] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+      } else {
+        const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
+        if (c < n_c) {
           a.part_m[pc] = m;
           a.part_l[pc] = sum;
         }
@@ -871,56 +930,68 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     __syncthreads();
     const int pitch = pl.n_v * 128, shift = a.voff - pl.v0 * 128;
     const bool vec = a.dv % 4 == 0 && shift % 4 == 0;
-    const uint32_t base = smem_u32(ring);
     const int mine = max(0, min(share, n_c - cs));
-    // A warp takes a column's values 128 at a time (four a lane); one value a lane where the
-    // value columns do not start or end on a multiple of four.
-    const int step = vec ? 128 : 32, per = (a.dv + step - 1) / step;
-    auto join_columns = [&](auto count) {
-      constexpr int kX = decltype(count)::value;
-#pragma unroll 2
-      for (int i = warp; i < mine * per; i += kThreads / 32) {
-        const int cl = i / per, v = (i - cl * per) * step + lane * (vec ? 4 : 1);
-        if (v >= a.dv) continue;
-        const uint32_t at = base + static_cast<uint32_t>(((cs + cl) * pitch + shift + v) * 4);
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-        if (vec) {
-          float4 f[kX];
+    float* part_o = a.part_o + ((((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol) + c_base + cs) * a.dv;
+    __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(a.out);
+    if (vec) {
+      // A warp keeps to 128 of a column's values (four a lane) and takes every few columns;
+      // several columns' loads are in flight.
+      const int per = (a.dv + 127) >> 7, lanes_of = (kThreads / 32) / per;   // 1 to 4 parts of a column
+      const int p = warp / lanes_of, first = warp - p * lanes_of, v = p * 128 + lane * 4;
+      auto join_columns = [&](auto count) {
+        constexpr int kX = decltype(count)::value, kMost = C == 32 ? 8 : 16;
+        constexpr int kItems = kMost / kX > 4 ? 4 : kMost / kX;
+        uint32_t from[kX];
 #pragma unroll
-          for (int x = 0; x < kX; ++x) f[x] = peer_ld4(peer(at, x));
+        for (int x = 0; x < kX; ++x) from[x] = peer(smem_u32(ring) + static_cast<uint32_t>((cs * pitch + shift + v) * 4), x);
+#pragma unroll 1
+        for (int cl = first; cl < mine; cl += kItems * lanes_of) {
+          float4 f[kItems][kX];
 #pragma unroll
-          for (int x = 0; x < kX; ++x) {
-            const float w = wtab[x * share + cl];
-            o[0] = fmaf(w, f[x].x, o[0]);
-            o[1] = fmaf(w, f[x].y, o[1]);
-            o[2] = fmaf(w, f[x].z, o[2]);
-            o[3] = fmaf(w, f[x].w, o[3]);
+          for (int k = 0; k < kItems; ++k) {
+            const uint32_t at = static_cast<uint32_t>(min(cl + k * lanes_of, mine - 1) * pitch * 4);
+#pragma unroll
+            for (int x = 0; x < kX; ++x) f[k][x] = peer_ld4(from[x] + at);
           }
-        } else {
-          for (int x = 0; x < kX; ++x) o[0] = fmaf(wtab[x * share + cl], peer_ld(peer(at, x)), o[0]);
+#pragma unroll
+          for (int k = 0; k < kItems; ++k) {
+            const int c = cl + k * lanes_of;
+            if (c >= mine) break;
+            float2 o0 = make_float2(0.f, 0.f), o1 = o0;
+#pragma unroll
+            for (int x = 0; x < kX; ++x) {
+              const float w = wtab[x * share + c];
+              o0 = fma2(make_float2(w, w), make_float2(f[k][x].x, f[k][x].y), o0);
+              o1 = fma2(make_float2(w, w), make_float2(f[k][x].z, f[k][x].w), o1);
+            }
+            if (a.splits == 1) {
+              const __nv_bfloat162 p0 = __floats2bfloat162_rn(o0.x, o0.y), p1 = __floats2bfloat162_rn(o1.x, o1.y);
+              *reinterpret_cast<uint2*>(outp + static_cast<size_t>(place[c]) * a.dv + v) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
+            } else {
+              *reinterpret_cast<float4*>(part_o + static_cast<size_t>(c) * a.dv + v) = make_float4(o0.x, o0.y, o1.x, o1.y);
+            }
+          }
         }
-        const int col = c_base + cs + cl;
-        if (a.splits == 1) {
-          const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + oc * a.dv + v;
-          if (vec) {
-            const __nv_bfloat162 p0 = __floats2bfloat162_rn(o[0], o[1]), p1 = __floats2bfloat162_rn(o[2], o[3]);
-            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&p0), *reinterpret_cast<const uint32_t*>(&p1));
-          } else {
-            out[0] = __float2bfloat16_rn(o[0]);
-          }
-        } else {
-          const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
-          if (vec) *reinterpret_cast<float4*>(a.part_o + pc * a.dv + v) = make_float4(o[0], o[1], o[2], o[3]);
-          else a.part_o[pc * a.dv + v] = o[0];
+      };
+      if (p < per && v < a.dv) {
+        switch (xl) {
+          case 0: join_columns(std::integral_constant<int, 1>{}); break;
+          case 1: join_columns(std::integral_constant<int, 2>{}); break;
+          case 2: join_columns(std::integral_constant<int, 4>{}); break;
+          default: join_columns(std::integral_constant<int, 8>{}); break;
         }
       }
-    };
-    switch (X) {
-      case 1: join_columns(std::integral_constant<int, 1>{}); break;
-      case 2: join_columns(std::integral_constant<int, 2>{}); break;
-      case 4: join_columns(std::integral_constant<int, 4>{}); break;
-      default: join_columns(std::integral_constant<int, 8>{}); break;
+    } else {
+      // value columns that do not start or end on a multiple of four: one a thread
+      for (int i = threadIdx.x; i < mine * a.dv; i += kThreads) {
+        const int c = i / a.dv, v = i - c * a.dv;
+        const uint32_t at = smem_u32(ring) + static_cast<uint32_t>(((cs + c) * pitch + shift + v) * 4);
+        float o = 0.f;
+        for (int x = 0; x < X; ++x) o = fmaf(wtab[x * share + c], peer_ld(peer(at, x)), o);
+        if (a.splits == 1) outp[static_cast<size_t>(place[c]) * a.dv + v] = __float2bfloat16_rn(o);
+        else part_o[static_cast<size_t>(c) * a.dv + v] = o;
+      }
     }
   }
   if (t.cluster > 1) cluster_sync();                       // nobody reads this block's shared memory any more
@@ -965,29 +1036,36 @@ bool kv_attend_tc_supported(long long max_tokens, int d, int dv, int voff, int q
   return p.n_v <= 4 && p.stages >= 2 && p.smem <= kSmemLimit;
 }
 
-void kv_attend_parts_tc(int B, int G, int ncol, long long max_tokens, int& cluster, int& groups) {
+void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups) {
   const int C = columns(ncol);
   const long long units = static_cast<long long>(B) * G * ((ncol + C - 1) / C);
   const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
   const long long least = (max_tokens + 16383) / 16384;   // parts, by the weights' range (see the top)
-  // A division costs its waves of blocks times a block's tiles, its start and end counted as three
-  // tiles (two blocks of an SM take its time in turn, so they count as two waves); a second kernel that joins clusters as three and their sums' traffic.  Clusters of 4
-  // and 8 leave some SMs of a graphics cluster unused.
-  const int xs[4] = {1, 2, 4, 8}, slots[4] = {148, 148, 144, 128};
-  long long best = -1;
+  // Blocks resident at once by cluster size (the occupancy calculator's answers on B200: clusters of
+  // 4 and 8 leave some SMs of a graphics cluster unused), twice that with two blocks an SM.
+  // A division costs the tiles of a block, its start and end counted as three, times: 1.5 for
+  // a block alone on an SM that could hold two, 2 for two of them, more by the waves; a second
+  // kernel that joins clusters as three tiles and their sums' traffic.
+  const int xs[4] = {1, 2, 4, 8}, slots[4] = {148, 148, 132, 120};
+  const double per_sm = C < 64 && plan_for(d, dv, voff, C).smem <= kSmemLimit / 2 - 1024 ? 2.0 : 1.0;
+  double best = -1.0;
   for (int k = 0; k < 4; ++k) {
-    const long long X = xs[k], room = slots[k];
+    const long long X = xs[k];
     if (X > 1 && X > tiles) break;
     for (long long gr = std::max<long long>(1, (least + X - 1) / X); gr <= 256; ++gr) {
-      if (best >= 0 && X * gr > tiles) break;
-      const long long waves = (units * gr * X + room - 1) / room;
-      const long long c = 16 * waves * ((tiles + X * gr - 1) / (X * gr) + 3) + (gr > 1 ? 48 + gr : 0) + 4 * k;
-      if (best < 0 || c < best) {
+      if (best >= 0.0 && X * gr > tiles) break;
+      const double blocks = static_cast<double>(units * gr * X), room = slots[k] * per_sm;
+      const double w = static_cast<double>((tiles + X * gr - 1) / (X * gr) + 3);
+      double c = blocks <= slots[k] ? w * (per_sm > 1.0 ? 1.5 : 1.0)
+                 : blocks <= room ? w * 2.2
+                                  : per_sm * w * (per_sm > 1.0 ? blocks / room + 0.25 : std::ceil(blocks / room));
+      c += (gr > 1 ? 3.0 + gr / 16.0 : 0.0) + 0.25 * k;
+      if (best < 0.0 || c < best) {
         best = c;
         cluster = static_cast<int>(X);
         groups = static_cast<int>(gr);
       }
-      if (units * gr * X > 16 * 148) break;
+      if (blocks > 16 * 148) break;
     }
   }
 }
@@ -999,6 +1077,7 @@ int launch_kv_attend_tc(const KvAttendArgs& a, int cluster, cudaStream_t s) {
   t.p = plan_for(a.d, a.dv, a.voff, C);
   t.col_groups = (ncol + C - 1) / C;
   t.cluster = cluster;
+  t.hg = a.H / a.g.G;
   const long long grid = static_cast<long long>(a.g.B) * a.g.G * a.splits * t.col_groups * cluster;
   // Rows of consecutive tokens follow one another within a page (a whole sequence without a table).
   CUtensorMap map{}, tail{};

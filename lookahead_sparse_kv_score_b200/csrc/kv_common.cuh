@@ -104,7 +104,7 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
 
 bool kv_attend_tc_supported(long long max_tokens, int d, int dv, int voff, int qdt, int ncol);
 // Blocks of a cluster and clusters of a unit (KvAttendArgs::splits) for the tensor-core path.
-void kv_attend_parts_tc(int B, int G, int ncol, long long max_tokens, int& cluster, int& groups);
+void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups);
 int launch_kv_attend_tc(const KvAttendArgs& a, int cluster, cudaStream_t s);
 int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens);
 int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s);
