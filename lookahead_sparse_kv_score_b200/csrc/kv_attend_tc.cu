@@ -26,9 +26,8 @@
 // multiplied by 2^(r_old - r_new) in tensor memory.  That is rare after the first tile, so the
 // cross-lane maxima are only computed then; otherwise a tile costs one vote.
 //
-// Roles (13 warps; 9 with 16 columns): warps 0-3 bring the rows, one token a lane, chunk by
-// chunk, and write the tokens' scales; warps 4-11 hold one token a lane and half of the
-// columns each; the last warp issues the MMAs, S a tile ahead of O, a chunk at a time as chunks
+// Roles (10, 14 or 22 warps by the columns): warps 0-3 bring the rows, one token a lane, chunk by
+// chunk, and write the tokens' scales; four warps for each 16 columns hold one token a lane; the last warp issues the MMAs, S a tile ahead of O, a chunk at a time as chunks
 // arrive.  A warp whose 32 rows follow one another in memory (a dense cache, pages of 16 and
 // more) brings them as TMA boxes; other rows (a fetched list) go by 16-byte asynchronous
 // copies in the MMA's swizzle, with zeros where a place has no token.  TMA row gathers were
@@ -59,13 +58,12 @@ using namespace tc;
 constexpr int kTile = 128;
 constexpr int kProducers = 128;               // warps 0-3
 
-// A block's shape by its query columns.  With 64 columns two groups of four warps hold half of
-// them each; with 16 one group holds all, and two blocks share an SM.
+// A block's shape by its query columns: a group of four weights warps (one a quadrant of the
+// tensor memory's lanes) for each 16 columns; up to 32 columns, two blocks share an SM.
+constexpr int NC = 16;                        // columns of a weights warp
 template <int C>
 struct Shape {
-  static constexpr int kGroups = C == 16 ? 1 : 2;
-  static constexpr int NC = C / kGroups;                   // columns of a weights warp
-  static constexpr int kWeights = 4 * kGroups;             // warps
+  static constexpr int kWeights = 4 * (C / NC);            // warps
   static constexpr int kMmaWarp = 4 + kWeights;            // the first of two: scores, values
   static constexpr int kThreads = 32 * (kMmaWarp + 2);
   static constexpr int kBlocks = C == 64 ? 1 : 2;          // blocks an SM, where shared memory allows
@@ -161,19 +159,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
                "%14, %15}, [%16];" : LSA_R8(r, 0), LSA_R8(r, 8) : "r"(t));
 }
-__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-               "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-               : LSA_R8(r, 0), LSA_R8(r, 8), LSA_R8(r, 16), LSA_R8(r, 24) : "r"(t));
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(t));
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(t) : "memory");
 }
 __device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
                "%13, %14, %15};" ::LSA_I8(r, 0), LSA_I8(r, 8), "r"(t) : "memory");
-}
-__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-               "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-               ::LSA_I8(r, 0), LSA_I8(r, 8), LSA_I8(r, 16), LSA_I8(r, 24), "r"(t) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -237,16 +231,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Whether the barrier's phase has completed, without waiting (try_wait may suspend the thread).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-// The MMA warp runs converged and an elected lane issues.  A descriptor's low word is made
+// The MMA warps run converged and an elected lane issues.  A descriptor's low word is made
 // uniform once a chunk, so that the ones behind it are sums in uniform registers: an MMA then
 // takes its 48 clocks (N = 64; 64 with N = 128, shared memory's rate), where descriptors in
 // vector registers made it 97.
@@ -313,7 +298,7 @@ __global__ void __launch_bounds__(Shape<C>::kThreads, Shape<C>::kBlocks)
 kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_tail,
                     const __grid_constant__ AttendTc t) {
   using Sh = Shape<C>;
-  constexpr int NC = Sh::NC, kMmaWarp = Sh::kMmaWarp, kThreads = Sh::kThreads;
+  constexpr int kMmaWarp = Sh::kMmaWarp, kThreads = Sh::kThreads;
   constexpr uint32_t kO = 4 * C;                           // tensor-memory columns: S (two of 2C), then O^T
   constexpr uint32_t kTmemCols = Sh::kTmemCols;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -384,6 +369,15 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+  // The query rows are on their way to L2 while the barriers are made.
+  if (warp >= 4 && warp < kMmaWarp) {
+    const int c = (warp - 4) * 4 + (lane >> 3), col = c_base + c, i = a.Tq == 1 ? 0 : col / hg;   // eight lanes a row
+    if (c < n_c) {
+      const char* qrow = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                       ((static_cast<size_t>(b) * a.Tq + i) * a.H + head * hg + (col - i * hg)) * a.d);
+      for (int e = (lane & 7) * 128; e < a.d * 2; e += 1024) asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + e));
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -463,9 +457,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
       const bool whole = __all_sync(0xffffffffu, there == 0xffu);
       const int row0 = __shfl_sync(0xffffffffu, row, 0), row16 = __shfl_sync(0xffffffffu, row, 16);
-      for (int c = 0; c <= pl.n_full && ok; ++c) {         // c = n_full: the tail
-        if (c == pl.n_full && !pl.tail) break;
-        const bool is_tail = c == pl.n_full;
+      // The chunks in order, the tail before the last of them: its slot is free earlier.
+      for (int step = 0; step < pl.n_full + pl.tail && ok; ++step) {
+        const bool is_tail = pl.tail && step == pl.n_full - 1;
+        const int c = pl.tail && step == pl.n_full ? step - 1 : step;
         const int slot = s * pl.n_full + c, col = (c < n_kf || is_tail ? (is_tail ? n_kf : c) : c + gap) * 128;
         uint64_t* full_bar = is_tail ? &tfull[ts] : &full[slot];
         ok = __all_sync(0xffffffffu, is_tail ? mbar_wait(&tempty[ts], tph ^ 1, abort_flag) : mbar_wait(&empty[slot], ph ^ 1, abort_flag));
@@ -689,7 +684,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-      asm volatile("barrier.cta.sync 3, %0;" ::"n"(32 * Sh::kWeights) : "memory");   // the columns' factors, to all
+      asm volatile("barrier.cta.sync 5, %0;" ::"n"(32 * Sh::kWeights) : "memory");   // the columns' factors, to all
     }
     // Scratch of 256 words for the group, in its own columns' bytes of the weights buffer (two
     // words a row), while no MMA reads them.
@@ -787,15 +782,26 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         if (quad == 0 && lane < NC) nref[c0 + lane] = now;
 #pragma unroll
         for (int c = 0; c < NC; ++c) (c & 1 ? l[c / 2].y : l[c / 2].x) *= __shfl_sync(0xffffffffu, f_mine, c);
+        const uint32_t moved = __ballot_sync(0xffffffffu, f_mine != 1.f);   // columns whose reference moved
         if (j > 0) {
 #pragma unroll 1
           for (int m = 0; m < pl.n_v; ++m) {
             const uint32_t at = tmem + lanes + kO + m * C + c0;
-            tmem_ld(at, hi);
-            tmem_wait_ld();
+            if (__popc(moved) > 4) {
+              tmem_ld(at, hi);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < NC; ++c) hi[c] = __float_as_uint(__uint_as_float(hi[c]) * __shfl_sync(0xffffffffu, f_mine, c));
-            tmem_st(at, hi);
+              for (int c = 0; c < NC; ++c) hi[c] = __float_as_uint(__uint_as_float(hi[c]) * __shfl_sync(0xffffffffu, f_mine, c));
+              tmem_st(at, hi);
+            } else {
+              for (uint32_t left = moved; left != 0; left &= left - 1) {
+                const int c = __ffs(left) - 1;
+                uint32_t o;
+                tmem_ld(at + c, o);
+                tmem_wait_ld();
+                tmem_st(at + c, __float_as_uint(__uint_as_float(o) * __shfl_sync(0xffffffffu, f_mine, c)));
+              }
+            }
           }
           tmem_wait_st();
         }
@@ -838,7 +844,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     // [C][128 n_v] fp32 (every tile has been read).
     if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
     tc_fence_after();
-    // Each step halves the columns a lane holds; lane l ends with column l (NC = 16: l / 2).
+    // Each step halves the columns a lane holds; lane l ends with column l / 2.
     float v[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
@@ -853,8 +859,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
       o >>= 1;
     }
-    if constexpr (NC == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-    *scratch(quad * 32 + (NC == 16 ? lane >> 1 : lane)) = v[0];
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+    *scratch(quad * 32 + (lane >> 1)) = v[0];
     group_sync(bar_id);
     if (quad == 0 && lane < NC)
       qf[c0 + lane] = (*scratch(lane) + *scratch(32 + lane)) + (*scratch(64 + lane) + *scratch(96 + lane));
@@ -939,8 +945,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       const int per = (a.dv + 127) >> 7, lanes_of = (kThreads / 32) / per;   // 1 to 4 parts of a column
       const int p = warp / lanes_of, first = warp - p * lanes_of, v = p * 128 + lane * 4;
       auto join_columns = [&](auto count) {
-        constexpr int kX = decltype(count)::value, kMost = C == 32 ? 8 : 16;
-        constexpr int kItems = kMost / kX > 4 ? 4 : kMost / kX;
+        constexpr int kX = decltype(count)::value, kItems = kX >= 8 ? 1 : 8 / kX > 4 ? 4 : 8 / kX;   // eight loads in flight
         uint32_t from[kX];
 #pragma unroll
         for (int x = 0; x < kX; ++x) from[x] = peer(smem_u32(ring) + static_cast<uint32_t>((cs * pitch + shift + v) * 4), x);
