@@ -203,75 +203,86 @@ def lsa_hot_pool_update(B, N, slots, row_bytes, trigger, U, cold_host, hot, stat
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _QTYPES = (torch.float32, torch.bfloat16)
+_I32, _F32, _F64, _U8 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.uint8,)
+
+
+def _bad(t, name, dtypes, n, device):
+    """Why a tensor cannot be passed on (the library would read it as it is)."""
+    if t.dtype not in dtypes:
+        return f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}"
+    if t.get_device() != device or device < 0:
+        return f"{name} is on {t.device}; every tensor of the call must be on one CUDA device"
+    if not t.is_contiguous():
+        return f"{name} of shape {tuple(t.shape)} with strides {t.stride()} is not contiguous"
+    return f"{name} has {t.numel()} elements, the call uses {n}"
 
 
 def _dev(t, name, dtypes, n, device):
     """Raw pointer of a dense device tensor of one of `dtypes` with at least n elements (None
-    -> NULL).  The library would read a host tensor, another type or a short array as it is."""
+    -> NULL); device: the CUDA device's index."""
     if t is None:
         return None
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}; every tensor of the call must be on one CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} of shape {tuple(t.shape)} with strides {t.stride()} is not contiguous")
-    if t.numel() < n:
-        raise ValueError(f"{name} has {t.numel()} elements, the call uses {n}")
-    return t.data_ptr()
+    if t.dtype in dtypes and t.get_device() == device >= 0 and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    raise ValueError(_bad(t, name, dtypes, n, device))
 
 
 def _dev_strided(t, name, dtypes, span, device):
     """As _dev for a view that the call walks with strides of its own: `span` elements from the
     view's first one must lie in its storage."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}; every tensor of the call must be on one CUDA device")
+    if t.dtype not in dtypes or t.get_device() != device or device < 0:
+        raise ValueError(_bad(t, name, dtypes, 0, device))
     if (t.storage_offset() + span) * t.element_size() > t.untyped_storage().nbytes():
         raise ValueError(f"{name}: {span} elements from its first one lie outside its storage")
     return t.data_ptr()
 
 
 def _call(fn, where, device, stream, *args):
-    """fn(*args, stream) with `device` current: its own current stream unless one is given."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
+    """fn(*args, stream) with `device` current, on that device's current stream unless one is
+    given."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)), where)
+            rc = fn(*args, stream)
+    if rc != LSA_OK:
+        _check(rc, where)
 
 
 def _kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, device):
     """The cache arguments common to the three calls, checked against the tensors' sizes."""
     if block < 1 or page < 1:
         raise ValueError(f"block = {block}, page = {page}: powers of two")
-    return (block, page, seq_pages, pages, _dev(table, "table", (torch.int32,), B * -(-N // page), device),
+    return (block, page, seq_pages, pages, _dev(table, "table", _I32, B * -(-N // page), device),
             _dev(rows, "rows", _CODES, pages * page * G * W, device),
-            _dev(scale, "scale", (torch.float32,), B * -(-N // block) * G, device))
+            _dev(scale, "scale", _F32, B * -(-N // block) * G, device))
 
 
 def lsa_kv_write(B, T, N, G, W, xdt, x, x_stride, start, count, block, page, seq_pages, pages, table, rows, scale,
                  status=None, stream=None):
-    d = x.device
+    d = x.get_device()
     if dtype_code(x) != xdt:
         raise ValueError(f"x is {x.dtype}, xdt {xdt}")
     _call(lib().lsa_kv_write, "lsa_kv_write", d, stream, B, T, N, G, W, xdt,
           _dev_strided(x, "x", _QTYPES, (B * T - 1) * x_stride + G * W if B * T > 0 else 0, d), x_stride,
-          _dev(start, "start", (torch.int32,), B, d), _dev(count, "count", (torch.int32,), B, d),
+          _dev(start, "start", _I32, B, d), _dev(count, "count", _I32, B, d),
           *_kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, d),
-          _dev(status, "status", (torch.int32,), 1, d))
+          _dev(status, "status", _I32, 1, d))
 
 
 def lsa_kv_read(B, N, G, W, idx, cap, count, block, page, seq_pages, pages, table, rows, scale, odt, out,
                 status=None, stream=None):
-    d = out.device
+    d = out.get_device()
     if dtype_code(out) != odt:
         raise ValueError(f"out is {out.dtype}, odt {odt}")
-    _call(lib().lsa_kv_read, "lsa_kv_read", d, stream, B, N, G, W, _dev(idx, "idx", (torch.int32,), B * cap, d), cap,
-          _dev(count, "count", (torch.int32,), B, d),
+    _call(lib().lsa_kv_read, "lsa_kv_read", d, stream, B, N, G, W, _dev(idx, "idx", _I32, B * cap, d), cap,
+          _dev(count, "count", _I32, B, d),
           *_kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, d), odt,
-          _dev(out, "out", _QTYPES, B * cap * G * W, d), _dev(status, "status", (torch.int32,), 1, d))
+          _dev(out, "out", _QTYPES, B * cap * G * W, d), _dev(status, "status", _I32, 1, d))
 
 
 def lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, window, cap) -> int:
@@ -280,27 +291,27 @@ def lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, wi
 
 def lsa_kv_attend(B, Tq, N, H, G, d, dv, voff, W, qdt, q, sm_scale, length, sinks, window, idx, cap, count, block,
                   page, seq_pages, pages, table, rows, scale, out, lse, workspace, status=None, stream=None):
-    dev = q.device
+    dev = q.get_device()
     if dtype_code(q) != qdt or out.dtype != q.dtype:
         raise ValueError(f"q is {q.dtype}, out {out.dtype}, qdt {qdt}")
-    i32 = (torch.int32,)
+    i32 = _I32
     _call(lib().lsa_kv_attend, "lsa_kv_attend", dev, stream, B, Tq, N, H, G, d, dv, voff, W, qdt,
           _dev(q, "q", _QTYPES, B * Tq * H * d, dev), float(sm_scale), _dev(length, "length", i32, B, dev), sinks,
           window, _dev(idx, "idx", i32, B * cap, dev), cap, _dev(count, "count", i32, B, dev),
           *_kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, dev),
-          _dev(out, "out", _QTYPES, B * Tq * H * dv, dev), _dev(lse, "lse", (torch.float32,), B * Tq * H, dev),
-          _dev(status, "status", i32, 1, dev), _dev(workspace, "workspace", (torch.uint8,), 0, dev),
+          _dev(out, "out", _QTYPES, B * Tq * H * dv, dev), _dev(lse, "lse", _F32, B * Tq * H, dev),
+          _dev(status, "status", i32, 1, dev), _dev(workspace, "workspace", _U8, 0, dev),
           0 if workspace is None else workspace.numel())
 
 
 def lsa_rope(R, H, rot, half, dt, x, x_token, x_head, pos, freq, mscale, inverse, out, o_token, o_head, stream=None):
-    d = x.device
+    d = x.get_device()
     if dtype_code(x) != dt or out.dtype != x.dtype:
         raise ValueError(f"x is {x.dtype}, out {out.dtype}, dt {dt}")
     span = lambda t, h: (R - 1) * t + (H - 1) * h + rot if R > 0 and H > 0 else 0  # noqa: E731
     _call(lib().lsa_rope, "lsa_rope", d, stream, R, H, rot, int(half), dt,
           _dev_strided(x, "x", _QTYPES, span(x_token, x_head), d), x_token, x_head,
-          _dev(pos, "pos", (torch.int32,), R, d), _dev(freq, "freq", (torch.float64,), rot // 2, d), float(mscale),
+          _dev(pos, "pos", _I32, R, d), _dev(freq, "freq", _F64, rot // 2, d), float(mscale),
           int(inverse), _dev_strided(out, "out", _QTYPES, span(o_token, o_head), d), o_token, o_head)
 
 

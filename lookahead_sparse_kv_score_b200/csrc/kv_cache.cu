@@ -16,23 +16,42 @@ namespace lsa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHold = 8;        // 8-element vectors a thread keeps in registers between the passes
 constexpr uint32_t kNanBits = 0x7fc00000u;
 
-// Eight consecutive elements as fp32 bits.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Eight consecutive elements as they lie in memory.
+struct Raw32 { uint4 a, b; };
+struct Raw16 { uint4 a; };
+__device__ __forceinline__ Raw32 load8(const float* p) {
+  return {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1)};
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ Raw16 load8(const __nv_bfloat16* p) { return {__ldg(reinterpret_cast<const uint4*>(p))}; }
+__device__ __forceinline__ void to_floats(const Raw32& r, float (&v)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void to_floats(const Raw16& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+// Largest magnitude as its bits: non-finite values have the largest of all.
+__device__ __forceinline__ uint32_t amax_bits(const Raw32& r) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+  return m;
+}
+__device__ __forceinline__ uint32_t amax_bits(const Raw16& r) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+  return m;
 }
 
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
@@ -50,14 +69,6 @@ __device__ __forceinline__ void decode2(uint32_t w, float s, float& a, float& b)
   b = f.y * s;
 }
 
-// Largest magnitude as its bits: non-finite values have the largest of all.
-__device__ __forceinline__ uint32_t amax_bits(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
-}
-
 // Bits of the smallest power of two s >= 2^-24 with amax / s <= 448 = 1.75 * 2^8.
 __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
   if (amax >= 0x7f800000u) return kNanBits;
@@ -65,19 +76,23 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
   return max(e, 127 - 24) << 23;
 }
 
-// One team of kTeam threads per (sequence, block of tokens, head) the call touches.
-template <typename T, int kTeam>
+// One team of kWarps warps per (sequence, block of tokens, head) the call touches.  A row of W
+// codes is read by 2^lpr lanes, eight elements each; the team's rows follow one another over
+// its lanes.  A thread keeps its first vectors in registers between the maximum and the
+// encoding, and reads what is behind them a second time (from L1 or L2).
+template <typename T, int kWarps>
 __global__ void __launch_bounds__(kThreads)
-kv_write_kernel(const KvGeom g, int n_new, int blocks_per_seq, const T* __restrict__ x, size_t x_stride,
+kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __restrict__ x, size_t x_stride, int lpr,
                 const int32_t* __restrict__ start, const int32_t* __restrict__ count, int32_t* status) {
+  using Raw = decltype(load8(static_cast<const T*>(nullptr)));
+  constexpr int kHold = sizeof(T) == 2 ? 9 : 5;
   __shared__ uint32_t red[kThreads / 32];
-  const int lane = threadIdx.x % kTeam;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / kTeam) + threadIdx.x / kTeam;
-  const long long units = static_cast<long long>(g.B) * blocks_per_seq * g.G;
-  if (unit >= units) return;           // whole teams leave (a block-wide team has one unit)
-  const int head = static_cast<int>(unit % g.G);
-  const long long ub = unit / g.G;
-  const int b = static_cast<int>(ub / blocks_per_seq), j = static_cast<int>(ub % blocks_per_seq);
+  const int lane = threadIdx.x & 31, team_warp = (threadIdx.x >> 5) % kWarps;
+  const uint32_t unit = blockIdx.x * (kThreads / 32 / kWarps) + (threadIdx.x >> 5) / kWarps;
+  if (unit >= static_cast<uint32_t>(g.B) * blocks_per_seq * g.G) return;   // whole teams leave (a block-wide team has one unit)
+  const uint32_t ub = g.G == 1 ? unit : unit / g.G;
+  const int head = static_cast<int>(unit - ub * g.G);
+  const int b = static_cast<int>(ub / blocks_per_seq), j = static_cast<int>(ub - b * blocks_per_seq);
   const int n = count != nullptr ? min(max(__ldg(count + b), 0), n_new) : n_new;
   const long long first = __ldg(start + b);
   const long long last = first + n;                              // one past the new tokens
@@ -90,82 +105,96 @@ kv_write_kernel(const KvGeom g, int n_new, int blocks_per_seq, const T* __restri
   const int lo = static_cast<int>(max(t0, first) - first);       // new tokens of this block
   const int hi = static_cast<int>(min(min(t0 + (1ll << g.block_log), last), static_cast<long long>(g.N)) - first);
   if (hi <= lo) return;
-  const int vpr = g.W / 8;
-  const int nv = (hi - lo) * vpr;
+  const int vpr = g.W / 8, rows = hi - lo;
+  const int step = kWarps << (5 - lpr);                          // rows of the team at a time
+  const int row0 = (team_warp << (5 - lpr)) + (lane >> lpr), col0 = lane & ((1 << lpr) - 1);
   const T* xb = x + (static_cast<size_t>(b) * n_new + lo) * x_stride + static_cast<size_t>(head) * g.W;
-  auto src = [&](int v) { const int i = v / vpr; return xb + static_cast<size_t>(i) * x_stride + (v - i * vpr) * 8; };
-
-  float held[kHold][8];
-  uint32_t m = 0;
-#pragma unroll
-  for (int k = 0; k < kHold; ++k) {
-    const int v = lane + k * kTeam;
-    if (v < nv) {
-      load8(src(v), held[k]);
-      m = max(m, amax_bits(held[k]));
-    }
-  }
-  for (int v = lane + kHold * kTeam; v < nv; v += kTeam) {
-    float f[8];
-    load8(src(v), f);
-    m = max(m, amax_bits(f));
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
-  if constexpr (kTeam > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x / 32] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = max(m, red[w]);
-  }
-  uint32_t sb = scale_bits(m);
   float* sp = g.scale + (static_cast<size_t>(b) * g.n_blocks + blk) * g.G + head;
   const bool grown_block = t0 < first;               // tokens before the new ones stay in the block
-  float before = 0.f;
+  const float before = grown_block ? *sp : 0.f;
+
+  // The thread's vectors in order: columns col0, col0 + 32, .. of rows row0, row0 + step, ..
+  auto next = [&](int& r, int& c) {
+    c += 32;
+    if (c >= vpr) {
+      c = col0;
+      r += step;
+    }
+  };
+  Raw held[kHold];
+  uint32_t m = 0;
+  int r = row0, c = col0;
+  if (col0 >= vpr) r = rows;                         // lanes past the row's end have none
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    if (r < rows) held[k] = load8(xb + static_cast<size_t>(r) * x_stride + c * 8);
+    next(r, c);
+  }
+  r = row0;
+  c = col0;
+  if (col0 >= vpr) r = rows;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    if (r < rows) m = max(m, amax_bits(held[k]));
+    next(r, c);
+  }
+  for (; r < rows; next(r, c)) m = max(m, amax_bits(load8(xb + static_cast<size_t>(r) * x_stride + c * 8)));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if constexpr (kWarps > 1) {
+    if (lane == 0) red[threadIdx.x / 32] = m;
+    __syncthreads();                                 // and every thread has read the old scale
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) m = max(m, red[w]);
+  } else {
+    __syncwarp();
+  }
+  uint32_t sb = scale_bits(m);
   if (grown_block) {
-    before = *sp;
     if (!(before <= 3.4e38f)) sb = kNanBits;
     else if (sb != kNanBits) sb = max(sb, __float_as_uint(max(before, 0.f)));
-    if constexpr (kTeam > 32) __syncthreads(); else __syncwarp();   // every thread has read the old scale
   }
   const float s = __uint_as_float(sb);
   const bool finite = sb != kNanBits;
   const float inv = finite ? 1.0f / s : 0.f;
-  if (lane == 0) *sp = s;
+  if (lane == 0 && team_warp == 0) *sp = s;
 
-  auto put = [&](int v, const float (&f)[8]) {
-    const int i = v / vpr;
-    const long long row = kv_row(g, b, static_cast<int>(first + lo + i));
-    if (row < 0) {
-      raise_status(status, LSA_ERR_RANGE);
-      return;
+  int row_of = -1;                                   // the row whose place is known
+  long long place = -1;
+  auto put = [&](int rr, int cc, const Raw& raw) {
+    if (rr != row_of) {
+      row_of = rr;
+      place = kv_row(g, b, static_cast<int>(first + lo + rr));
+      if (place < 0) raise_status(status, LSA_ERR_RANGE);
     }
+    if (place < 0) return;
+    float f[8];
+    to_floats(raw, f);
     const uint2 code = finite ? encode8(f, inv) : make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(g.rows + (static_cast<size_t>(row) * g.G + head) * g.W + (v - i * vpr) * 8) = code;
+    *reinterpret_cast<uint2*>(g.rows + (static_cast<size_t>(place) * g.G + head) * g.W + cc * 8) = code;
   };
+  r = row0;
+  c = col0;
+  if (col0 >= vpr) r = rows;
 #pragma unroll
   for (int k = 0; k < kHold; ++k) {
-    const int v = lane + k * kTeam;
-    if (v < nv) put(v, held[k]);
+    if (r < rows) put(r, c, held[k]);
+    next(r, c);
   }
-  for (int v = lane + kHold * kTeam; v < nv; v += kTeam) {
-    float f[8];
-    load8(src(v), f);
-    put(v, f);
-  }
+  for (; r < rows; next(r, c)) put(r, c, load8(xb + static_cast<size_t>(r) * x_stride + c * 8));
   if (grown_block && !(before == s)) {
     const float ratio = finite ? before * inv : 0.f;
     const int n_old = static_cast<int>(first - t0) * vpr;
-    for (int v = lane; v < n_old; v += kTeam) {
+    for (int v = team_warp * 32 + lane; v < n_old; v += kWarps * 32) {
       const int i = v / vpr;
       const long long row = kv_row(g, b, static_cast<int>(t0 + i));
       if (row < 0) continue;
       uint2* p = reinterpret_cast<uint2*>(g.rows + (static_cast<size_t>(row) * g.G + head) * g.W + (v - i * vpr) * 8);
-      const uint2 c = *p;
+      const uint2 code = *p;
       float f[8];
-      decode2(c.x & 0xffffu, 1.f, f[0], f[1]);
-      decode2(c.x >> 16, 1.f, f[2], f[3]);
-      decode2(c.y & 0xffffu, 1.f, f[4], f[5]);
-      decode2(c.y >> 16, 1.f, f[6], f[7]);
+      decode2(code.x & 0xffffu, 1.f, f[0], f[1]);
+      decode2(code.x >> 16, 1.f, f[2], f[3]);
+      decode2(code.y & 0xffffu, 1.f, f[4], f[5]);
+      decode2(code.y >> 16, 1.f, f[6], f[7]);
       *p = finite ? encode8(f, ratio) : make_uint2(0u, 0u);
     }
   }
@@ -185,35 +214,58 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Thread per eight codes of one listed token's rows.
+// Sixteen codes of a listed token a thread, kItems of them in flight: their list entries, then
+// their pages and scales, then their codes.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 kv_read_kernel(const KvGeom g, const int32_t* __restrict__ idx, int cap, const int32_t* __restrict__ count,
-               T* __restrict__ out, int32_t* status) {
-  const int vpt = g.G * (g.W / 8);                 // vectors of one token
-  const long long per_seq = static_cast<long long>(cap) * vpt, all = per_seq * g.B;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < all;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const int b = static_cast<int>(i / per_seq);
-    const long long r = i - b * per_seq;
-    const int j = static_cast<int>(r / vpt), v = static_cast<int>(r - static_cast<long long>(j) * vpt);
-    if (count != nullptr && j >= __ldg(count + b)) continue;
-    const int t = idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j) : j;
-    if (t < 0) continue;
-    const long long row = t < g.N ? kv_row(g, b, t) : -1;
-    if (row < 0) {
-      raise_status(status, LSA_ERR_RANGE);
-      continue;
+               T* __restrict__ out, int32_t* status, uint32_t blocks_per_seq) {
+  constexpr int kItems = 4;
+  const uint32_t vpr = g.W / 16, vpt = g.G * vpr;  // vectors of a row and of a token
+  const uint32_t b = blockIdx.x / blocks_per_seq;
+  const unsigned long long i0 = static_cast<unsigned long long>(blockIdx.x - b * blocks_per_seq) * (kThreads * kItems) + threadIdx.x;
+  const int n = count != nullptr ? min(max(__ldg(count + b), 0), cap) : cap;
+  int tok[kItems];
+  uint32_t at[kItems];                             // vector of the token
+  size_t to[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const unsigned long long i = i0 + k * kThreads;
+    const uint32_t j = vpt == 1 ? static_cast<uint32_t>(i)
+                       : i >> 32 ? static_cast<uint32_t>(i / vpt) : static_cast<uint32_t>(i) / vpt;
+    at[k] = static_cast<uint32_t>(i - static_cast<unsigned long long>(j) * vpt);
+    to[k] = (static_cast<size_t>(b) * cap + j) * vpt + at[k];
+    tok[k] = i < static_cast<unsigned long long>(cap) * vpt && j < static_cast<uint32_t>(n)
+                 ? (idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j) : static_cast<int>(j)) : -1;
+  }
+  long long row[kItems];
+  float s[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    row[k] = -1;
+    s[k] = 0.f;
+    if (tok[k] < 0) continue;
+    if (tok[k] < g.N) {
+      row[k] = kv_row(g, b, tok[k]);
+      s[k] = __ldg(g.scale + kv_scale_at(g, b, tok[k], g.G == 1 ? 0 : at[k] / vpr));
     }
-    const int head = v / (g.W / 8);
-    const float s = __ldg(g.scale + kv_scale_at(g, b, t, head));
-    const uint2 c = *reinterpret_cast<const uint2*>(g.rows + static_cast<size_t>(row) * g.G * g.W + v * 8);
-    float f[8];
-    decode2(c.x & 0xffffu, s, f[0], f[1]);
-    decode2(c.x >> 16, s, f[2], f[3]);
-    decode2(c.y & 0xffffu, s, f[4], f[5]);
-    decode2(c.y >> 16, s, f[6], f[7]);
-    store8(out + static_cast<size_t>(i) * 8, f);
+    if (row[k] < 0) raise_status(status, LSA_ERR_RANGE);
+  }
+  uint4 c[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k)
+    if (row[k] >= 0) c[k] = *reinterpret_cast<const uint4*>(g.rows + (static_cast<size_t>(row[k]) * vpt + at[k]) * 16);
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (row[k] < 0) continue;
+    const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) decode2((w[2 * h + e / 2] >> (16 * (e & 1))) & 0xffffu, s[k], f[2 * e], f[2 * e + 1]);
+      store8(out + to[k] * 16 + h * 8, f);
+    }
   }
 }
 
@@ -221,14 +273,17 @@ template <typename T>
 void write_typed(const KvGeom& g, int n_new, int per_seq, const void* x, size_t x_stride, const int32_t* start,
                  const int32_t* count, int32_t* status, cudaStream_t s) {
   const long long units = static_cast<long long>(g.B) * per_seq * g.G;
-  const long long vectors = (static_cast<long long>(std::min(1 << g.block_log, n_new))) * (g.W / 8);
-  // A warp keeps up to 256 vectors of its unit in registers; larger units get a whole block.
-  if (vectors <= 32 * kHold) {
-    kv_write_kernel<T, 32><<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, s>>>(
-        g, n_new, per_seq, static_cast<const T*>(x), x_stride, start, count, status);
+  const int vpr = g.W / 8, rows = std::min(1 << g.block_log, n_new);
+  int lpr = 0;
+  while (lpr < 5 && (1 << lpr) < vpr) ++lpr;
+  // A warp takes a unit whose vectors its lanes can hold, a block of eight warps a larger one.
+  const int per_lane = ((rows << lpr) + 31) / 32 * ((vpr + 31) / 32);
+  if (per_lane <= (sizeof(T) == 2 ? 9 : 5)) {
+    kv_write_kernel<T, 1><<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, s>>>(
+        g, n_new, per_seq, static_cast<const T*>(x), x_stride, lpr, start, count, status);
   } else {
-    kv_write_kernel<T, kThreads><<<static_cast<unsigned>(units), kThreads, 0, s>>>(
-        g, n_new, per_seq, static_cast<const T*>(x), x_stride, start, count, status);
+    kv_write_kernel<T, kThreads / 32><<<static_cast<unsigned>(units), kThreads, 0, s>>>(
+        g, n_new, per_seq, static_cast<const T*>(x), x_stride, lpr, start, count, status);
   }
 }
 
@@ -245,10 +300,12 @@ int launch_kv_write(const KvGeom& g, int T, int xdt, const void* x, size_t x_str
 
 int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* count, int odt, void* out,
                    int32_t* status, cudaStream_t s) {
-  const long long all = static_cast<long long>(g.B) * cap * g.G * (g.W / 8);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>((all + kThreads - 1) / kThreads, 1 << 30));
-  if (odt == LSA_F32) kv_read_kernel<float><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status);
-  else kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status);
+  const long long per_seq = (static_cast<long long>(cap) * g.G * (g.W / 16) + 4 * kThreads - 1) / (4 * kThreads);
+  if (per_seq * g.B > 0x7fffffffll)
+    return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap * G * W = %lld (at most 2^45)", static_cast<long long>(g.B) * cap * g.G * g.W);
+  const unsigned grid = static_cast<unsigned>(per_seq * g.B);
+  if (odt == LSA_F32) kv_read_kernel<float><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, static_cast<uint32_t>(per_seq));
+  else kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, static_cast<uint32_t>(per_seq));
   return check_launch("kv_read");
 }
 

@@ -105,6 +105,6 @@ def test_binding_refuses_host_tensors_types_and_short_arrays(lib):
     with pytest.raises(ValueError, match="xdt"):
         lsa.lsa_kv_write(2, 4, 64, 2, 32, 0, x, 64, i, None, 4, 4, 16, 32, None, rows, scale, stream=0)
     with pytest.raises(ValueError, match="expected"):
-        lsa._dev(torch.zeros(4, dtype=torch.int64), "idx", (torch.int32,), 4, torch.device("cpu"))
+        lsa._dev(torch.zeros(4, dtype=torch.int64), "idx", (torch.int32,), 4, 0)
     with pytest.raises(ValueError, match="one CUDA device"):
         lsa.lsa_rope(2, 1, 8, 0, 1, x, 64, 8, i, torch.zeros(4, dtype=torch.float64), 1.0, 0, x, 64, 8, stream=0)
