@@ -46,12 +46,10 @@ __device__ __forceinline__ uint32_t amax_bits(const Raw32& r) {
   for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
   return m;
 }
-__device__ __forceinline__ uint32_t amax_bits(const Raw16& r) {
-  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
-  return m;
+__device__ __forceinline__ uint32_t amax_bits(const Raw16& r) {      // two 16-bit maxima an instruction
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(r.a.x & k, r.a.y & k), __vmaxu2(r.a.z & k, r.a.w & k));
+  return max(m << 16, m & 0xffff0000u);
 }
 
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
@@ -81,7 +79,7 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
 // its lanes.  A thread keeps its first vectors in registers between the maximum and the
 // encoding, and reads what is behind them a second time (from L1 or L2).
 template <typename T, int kWarps>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __restrict__ x, size_t x_stride, int lpr,
                 const int32_t* __restrict__ start, const int32_t* __restrict__ count, int32_t* status) {
   using Raw = decltype(load8(static_cast<const T*>(nullptr)));
@@ -106,39 +104,43 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
   const int hi = static_cast<int>(min(min(t0 + (1ll << g.block_log), last), static_cast<long long>(g.N)) - first);
   if (hi <= lo) return;
   const int vpr = g.W / 8, rows = hi - lo;
-  const int step = kWarps << (5 - lpr);                          // rows of the team at a time
+  const int step_log = (kWarps == 8 ? 8 : 5) - lpr;              // rows of the team at a time
   const int row0 = (team_warp << (5 - lpr)) + (lane >> lpr), col0 = lane & ((1 << lpr) - 1);
   const T* xb = x + (static_cast<size_t>(b) * n_new + lo) * x_stride + static_cast<size_t>(head) * g.W;
   float* sp = g.scale + (static_cast<size_t>(b) * g.n_blocks + blk) * g.G + head;
   const bool grown_block = t0 < first;               // tokens before the new ones stay in the block
   const float before = grown_block ? *sp : 0.f;
 
-  // The thread's vectors in order: columns col0, col0 + 32, .. of rows row0, row0 + step, ..
-  auto next = [&](int& r, int& c) {
-    c += 32;
-    if (c >= vpr) {
-      c = col0;
-      r += step;
+  // The thread's vectors: rows row0, row0 + step, .. of column col0, then of column col0 + 32, ..
+  const int nr = rows > row0 ? (rows - row0 + (1 << step_log) - 1) >> step_log : 0;
+  const int nv = nr * (col0 < vpr ? (vpr - col0 + 31) >> 5 : 0);
+  const size_t x_step = x_stride << step_log;
+  const T* xp = xb + static_cast<size_t>(row0) * x_stride + col0 * 8;
+  auto next_x = [&](int& left, const T*& p) {        // left: rows of this column from here on
+    p += x_step;
+    if (--left == 0) {
+      left = nr;
+      p += 256;
+      p -= x_step * nr;
     }
   };
   Raw held[kHold];
   uint32_t m = 0;
-  int r = row0, c = col0;
-  if (col0 >= vpr) r = rows;                         // lanes past the row's end have none
+  int left = nr;
+  const T* p = xp;
 #pragma unroll
-  for (int k = 0; k < kHold; ++k) {
-    if (r < rows) held[k] = load8(xb + static_cast<size_t>(r) * x_stride + c * 8);
-    next(r, c);
-  }
-  r = row0;
-  c = col0;
-  if (col0 >= vpr) r = rows;
+  for (int k = 0; k < kHold; ++k)
+    if (k < nv) {
+      held[k] = load8(p);
+      next_x(left, p);
+    }
 #pragma unroll
-  for (int k = 0; k < kHold; ++k) {
-    if (r < rows) m = max(m, amax_bits(held[k]));
-    next(r, c);
+  for (int k = 0; k < kHold; ++k)
+    if (k < nv) m = max(m, amax_bits(held[k]));
+  for (int k = kHold; k < nv; ++k) {
+    m = max(m, amax_bits(load8(p)));
+    next_x(left, p);
   }
-  for (; r < rows; next(r, c)) m = max(m, amax_bits(load8(xb + static_cast<size_t>(r) * x_stride + c * 8)));
   m = __reduce_max_sync(0xffffffffu, m);
   if constexpr (kWarps > 1) {
     if (lane == 0) red[threadIdx.x / 32] = m;
@@ -158,29 +160,60 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
   const float inv = finite ? 1.0f / s : 0.f;
   if (lane == 0 && team_warp == 0) *sp = s;
 
-  int row_of = -1;                                   // the row whose place is known
-  long long place = -1;
-  auto put = [&](int rr, int cc, const Raw& raw) {
-    if (rr != row_of) {
-      row_of = rr;
-      place = kv_row(g, b, static_cast<int>(first + lo + rr));
-      if (place < 0) raise_status(status, LSA_ERR_RANGE);
-    }
-    if (place < 0) return;
-    float f[8];
-    to_floats(raw, f);
-    const uint2 code = finite ? encode8(f, inv) : make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(g.rows + (static_cast<size_t>(place) * g.G + head) * g.W + cc * 8) = code;
-  };
-  r = row0;
-  c = col0;
-  if (col0 >= vpr) r = rows;
+  // A block of tokens lies in one page unless pages are smaller; then each row is looked up.
+  const bool one_page = g.page_log >= g.block_log;
+  const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
+  uint8_t* const base = g.rows + static_cast<size_t>(head) * g.W + col0 * 8;
+  const int t_new = static_cast<int>(first) + lo;    // the team's first token
+  const long long place0 = one_page ? kv_row(g, b, t_new) : 0;
+  if (one_page && place0 < 0) {
+    raise_status(status, LSA_ERR_RANGE);
+  } else {
+    uint8_t* dst = base + static_cast<size_t>(place0 + row0) * row_bytes;
+    const size_t d_step = row_bytes << step_log;
+    int r = row0, col = 0;
+    auto put = [&](const Raw& raw) {
+      bool there = true;
+      if (!one_page) {
+        const long long place = kv_row(g, b, t_new + r);
+        there = place >= 0;
+        if (!there) raise_status(status, LSA_ERR_RANGE);
+        dst = base + static_cast<size_t>(there ? place : 0) * row_bytes + col;
+      }
+      if (there) {
+        float f[8];
+        to_floats(raw, f);
+        *reinterpret_cast<uint2*>(dst) = finite ? encode8(f, inv) : make_uint2(0u, 0u);
+      }
+    };
+    auto next_d = [&]() {
+      dst += d_step;
+      r += 1 << step_log;
+      if (r >= rows) {
+        r = row0;
+        col += 256;
+        dst += 256;
+        dst -= d_step * nr;
+      }
+    };
 #pragma unroll
-  for (int k = 0; k < kHold; ++k) {
-    if (r < rows) put(r, c, held[k]);
-    next(r, c);
+    for (int k = 0; k < kHold; ++k)
+      if (k < nv) {
+        put(held[k]);
+        next_d();
+      }
+    if (nv > kHold) {                                // from L1 or L2 again
+      left = nr;
+      p = xp;
+      for (int k = 0; k < nv; ++k) {
+        if (k >= kHold) {
+          put(load8(p));
+          next_d();
+        }
+        next_x(left, p);
+      }
+    }
   }
-  for (; r < rows; next(r, c)) put(r, c, load8(xb + static_cast<size_t>(r) * x_stride + c * 8));
   if (grown_block && !(before == s)) {
     const float ratio = finite ? before * inv : 0.f;
     const int n_old = static_cast<int>(first - t0) * vpr;
@@ -214,57 +247,64 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Sixteen codes of a listed token a thread, kItems of them in flight: their list entries, then
-// their pages and scales, then their codes.
+// A warp reads 2^tpw_log listed tokens.  Its lanes look the tokens up first (list entry, page and,
+// with one head, scale), then take the tokens' rows together, eight codes a lane (16 bytes of
+// bf16 out, so that a warp's stores are whole sectors), four in flight.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 kv_read_kernel(const KvGeom g, const int32_t* __restrict__ idx, int cap, const int32_t* __restrict__ count,
-               T* __restrict__ out, int32_t* status, uint32_t blocks_per_seq) {
-  constexpr int kItems = 4;
-  const uint32_t vpr = g.W / 16, vpt = g.G * vpr;  // vectors of a row and of a token
-  const uint32_t b = blockIdx.x / blocks_per_seq;
-  const unsigned long long i0 = static_cast<unsigned long long>(blockIdx.x - b * blocks_per_seq) * (kThreads * kItems) + threadIdx.x;
+               T* __restrict__ out, int32_t* status, uint32_t warps_per_seq, int tpw_log) {
+  const uint32_t vpr = g.W / 8, vpt = g.G * vpr;   // vectors of a row and of a token
+  const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const uint32_t b = warp / warps_per_seq;
+  if (b >= static_cast<uint32_t>(g.B)) return;
   const int n = count != nullptr ? min(max(__ldg(count + b), 0), cap) : cap;
-  int tok[kItems];
-  uint32_t at[kItems];                             // vector of the token
-  size_t to[kItems];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const unsigned long long i = i0 + k * kThreads;
-    const uint32_t j = vpt == 1 ? static_cast<uint32_t>(i)
-                       : i >> 32 ? static_cast<uint32_t>(i / vpt) : static_cast<uint32_t>(i) / vpt;
-    at[k] = static_cast<uint32_t>(i - static_cast<unsigned long long>(j) * vpt);
-    to[k] = (static_cast<size_t>(b) * cap + j) * vpt + at[k];
-    tok[k] = i < static_cast<unsigned long long>(cap) * vpt && j < static_cast<uint32_t>(n)
-                 ? (idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j) : static_cast<int>(j)) : -1;
-  }
-  long long row[kItems];
-  float s[kItems];
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    row[k] = -1;
-    s[k] = 0.f;
-    if (tok[k] < 0) continue;
-    if (tok[k] < g.N) {
-      row[k] = kv_row(g, b, tok[k]);
-      s[k] = __ldg(g.scale + kv_scale_at(g, b, tok[k], g.G == 1 ? 0 : at[k] / vpr));
+  const int j0 = static_cast<int>((warp - b * warps_per_seq) << tpw_log);
+  const int mine = min(1 << tpw_log, n - j0);      // tokens of this warp; what lies behind the count is left alone
+  if (mine <= 0) return;
+  int tok = -1, row = -1;
+  float scale = 0.f;
+  if (static_cast<int>(lane) < mine) {
+    tok = idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j0 + lane) : j0 + static_cast<int>(lane);
+    if (tok >= 0) {
+      if (tok < g.N) {
+        row = static_cast<int>(kv_row(g, b, tok));
+        scale = __ldg(g.scale + kv_scale_at(g, b, tok, 0));
+      }
+      if (row < 0) raise_status(status, LSA_ERR_RANGE);
     }
-    if (row[k] < 0) raise_status(status, LSA_ERR_RANGE);
   }
-  uint4 c[kItems];
+  T* const to = out + (static_cast<size_t>(b) * cap + j0) * vpt * 8 + lane * 8;
+  const uint32_t total = mine * vpt;
+  uint32_t tk = 0, c = lane;                       // token of this lane's vector, and the vector in it
+  while (c >= vpt) { c -= vpt; ++tk; }
+  for (uint32_t v0 = 0; v0 < total; v0 += 128) {
+    uint2 code[4];
+    float s[4];
+    bool there[4];
 #pragma unroll
-  for (int k = 0; k < kItems; ++k)
-    if (row[k] >= 0) c[k] = *reinterpret_cast<const uint4*>(g.rows + (static_cast<size_t>(row[k]) * vpt + at[k]) * 16);
+    for (int k = 0; k < 4; ++k) {
+      const int from = min(tk, 31u);
+      const int r = __shfl_sync(0xffffffffu, row, from);
+      s[k] = __shfl_sync(0xffffffffu, scale, from);
+      const int t = __shfl_sync(0xffffffffu, tok, from);
+      there[k] = v0 + k * 32 + lane < total && r >= 0;
+      if (there[k]) {
+        if (g.G > 1) s[k] = __ldg(g.scale + kv_scale_at(g, b, t, c / vpr));
+        code[k] = *reinterpret_cast<const uint2*>(g.rows + (static_cast<size_t>(r) * vpt + c) * 8);
+      }
+      c += 32;
+      while (c >= vpt) { c -= vpt; ++tk; }
+    }
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    if (row[k] < 0) continue;
-    const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int k = 0; k < 4; ++k) {
+      if (!there[k]) continue;
       float f[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) decode2((w[2 * h + e / 2] >> (16 * (e & 1))) & 0xffffu, s[k], f[2 * e], f[2 * e + 1]);
-      store8(out + to[k] * 16 + h * 8, f);
+      decode2(code[k].x & 0xffffu, s[k], f[0], f[1]);
+      decode2(code[k].x >> 16, s[k], f[2], f[3]);
+      decode2(code[k].y & 0xffffu, s[k], f[4], f[5]);
+      decode2(code[k].y >> 16, s[k], f[6], f[7]);
+      store8(to + static_cast<size_t>(v0 + k * 32) * 8, f);
     }
   }
 }
@@ -300,12 +340,15 @@ int launch_kv_write(const KvGeom& g, int T, int xdt, const void* x, size_t x_str
 
 int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* count, int odt, void* out,
                    int32_t* status, cudaStream_t s) {
-  const long long per_seq = (static_cast<long long>(cap) * g.G * (g.W / 16) + 4 * kThreads - 1) / (4 * kThreads);
-  if (per_seq * g.B > 0x7fffffffll)
-    return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap * G * W = %lld (at most 2^45)", static_cast<long long>(g.B) * cap * g.G * g.W);
-  const unsigned grid = static_cast<unsigned>(per_seq * g.B);
-  if (odt == LSA_F32) kv_read_kernel<float><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, static_cast<uint32_t>(per_seq));
-  else kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, static_cast<uint32_t>(per_seq));
+  // As many tokens a warp (up to 8) as leave about 32 warps for each SM.
+  int tpw = 0;
+  while (tpw < 3 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 32 * 148) ++tpw;
+  const long long per_seq = (cap + (1ll << tpw) - 1) >> tpw, warps = per_seq * g.B;
+  if (warps > 0x7fffffffll || static_cast<long long>(g.G) * (g.W / 8) > (1 << 24))
+    return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap = %lld, G * W = %lld (at most 2^31, 2^27)", static_cast<long long>(g.B) * cap, static_cast<long long>(g.G) * g.W);
+  const unsigned grid = static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)), ps = static_cast<unsigned>(per_seq);
+  if (odt == LSA_F32) kv_read_kernel<float><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);
+  else kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, ps, tpw);
   return check_launch("kv_read");
 }
 
