@@ -77,8 +77,10 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
 // One team of kWarps warps per (sequence, block of tokens, head) the call touches.  A row of W
 // codes is read by 2^lpr lanes, eight elements each; the team's rows follow one another over
 // its lanes.  A thread keeps its first vectors in registers between the maximum and the
-// encoding, and reads what is behind them a second time (from L1 or L2).
-template <typename T, int kWarps>
+// encoding, and reads what is behind them a second time (from L1 or L2).  kSimple: one column a
+// lane, at most kHold vectors and one page a block, which spares a third of the instructions
+// (the kernel is bound by their issue before it is by memory).
+template <typename T, int kWarps, bool kSimple>
 __global__ void __launch_bounds__(kThreads, 4)
 kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __restrict__ x, size_t x_stride, int lpr,
                 const int32_t* __restrict__ start, const int32_t* __restrict__ count, int32_t* status) {
@@ -131,13 +133,17 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
     if (k < nv) {
-      held[k] = load8(p);
-      next_x(left, p);
+      if constexpr (kSimple) {
+        held[k] = load8(xp + k * x_step);
+      } else {
+        held[k] = load8(p);
+        next_x(left, p);
+      }
     }
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
     if (k < nv) m = max(m, amax_bits(held[k]));
-  for (int k = kHold; k < nv; ++k) {
+  for (int k = kHold; !kSimple && k < nv; ++k) {
     m = max(m, amax_bits(load8(p)));
     next_x(left, p);
   }
@@ -196,13 +202,23 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
         dst -= d_step * nr;
       }
     };
+    if constexpr (kSimple) {
 #pragma unroll
-    for (int k = 0; k < kHold; ++k)
-      if (k < nv) {
-        put(held[k]);
-        next_d();
-      }
-    if (nv > kHold) {                                // from L1 or L2 again
+      for (int k = 0; k < kHold; ++k)
+        if (k < nv) {
+          float f[8];
+          to_floats(held[k], f);
+          *reinterpret_cast<uint2*>(dst + k * d_step) = finite ? encode8(f, inv) : make_uint2(0u, 0u);
+        }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kHold; ++k)
+        if (k < nv) {
+          put(held[k]);
+          next_d();
+        }
+    }
+    if (!kSimple && nv > kHold) {                                // from L1 or L2 again
       left = nr;
       p = xp;
       for (int k = 0; k < nv; ++k) {
@@ -318,13 +334,18 @@ void write_typed(const KvGeom& g, int n_new, int per_seq, const void* x, size_t 
   while (lpr < 5 && (1 << lpr) < vpr) ++lpr;
   // A warp takes a unit whose vectors its lanes can hold, a block of eight warps a larger one.
   const int per_lane = ((rows << lpr) + 31) / 32 * ((vpr + 31) / 32);
-  if (per_lane <= (sizeof(T) == 2 ? 9 : 5)) {
-    kv_write_kernel<T, 1><<<static_cast<unsigned>((units + 7) / 8), kThreads, 0, s>>>(
-        g, n_new, per_seq, static_cast<const T*>(x), x_stride, lpr, start, count, status);
-  } else {
-    kv_write_kernel<T, kThreads / 32><<<static_cast<unsigned>(units), kThreads, 0, s>>>(
-        g, n_new, per_seq, static_cast<const T*>(x), x_stride, lpr, start, count, status);
-  }
+  const int hold = sizeof(T) == 2 ? 9 : 5, team_lane = ((rows << lpr) + 255) / 256;   // vectors a lane of eight warps, one column
+  const bool simple = vpr <= 32 && g.page_log >= g.block_log;
+  const unsigned small = static_cast<unsigned>((units + 7) / 8), large = static_cast<unsigned>(units);
+  const T* xt = static_cast<const T*>(x);
+  if (per_lane <= hold && simple)
+    kv_write_kernel<T, 1, true><<<small, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
+  else if (per_lane <= hold)
+    kv_write_kernel<T, 1, false><<<small, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
+  else if (team_lane <= hold && simple)
+    kv_write_kernel<T, 8, true><<<large, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
+  else
+    kv_write_kernel<T, 8, false><<<large, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
 }
 
 }  // namespace
@@ -340,9 +361,10 @@ int launch_kv_write(const KvGeom& g, int T, int xdt, const void* x, size_t x_str
 
 int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* count, int odt, void* out,
                    int32_t* status, cudaStream_t s) {
-  // As many tokens a warp (up to 8) as leave about 32 warps for each SM.
+  // As many tokens a warp (up to 8) as leave 64 warps for each SM (65536 rows: 23.4 us with 4 tokens a
+  // warp, 25.2 with 2 and with 8, 29.8 with one).
   int tpw = 0;
-  while (tpw < 3 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 32 * 148) ++tpw;
+  while (tpw < 3 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 64 * 148) ++tpw;
   const long long per_seq = (cap + (1ll << tpw) - 1) >> tpw, warps = per_seq * g.B;
   if (warps > 0x7fffffffll || static_cast<long long>(g.G) * (g.W / 8) > (1 << 24))
     return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap = %lld, G * W = %lld (at most 2^31, 2^27)", static_cast<long long>(g.B) * cap, static_cast<long long>(g.G) * g.W);
