@@ -17,9 +17,7 @@ namespace lsa {
 namespace {
 
 constexpr int kTile = 32;          // tokens of a tile: one per lane for the scores
-constexpr int kWarps = 4;
-constexpr int kCols = 2;           // columns of a warp
-constexpr int kBlockCols = kWarps * kCols;
+constexpr int kWarps = 8;          // a column each
 constexpr int kMaxVpl = 16;        // value columns per lane (dv <= 512)
 
 __device__ __forceinline__ void store_out(void* out, int qdt, size_t i, float v) {
@@ -27,18 +25,23 @@ __device__ __forceinline__ void store_out(void* out, int qdt, size_t i, float v)
   else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
 }
 
+// kVec: value columns start and end on multiples of four, so that a lane holds four
+// neighbouring ones (16-byte shared loads); else every 32nd.
+template <bool kVec>
 __global__ void __launch_bounds__(kWarps * 32)
 kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) float smem[];
   const KvGeom& g = a.g;
-  const int pitch = rows_used | 1;                 // odd: a lane per token reads without conflicts
+  const int pitch = (rows_used + 31) / 32 * 32 + 4;   // a lane per token reads 16 bytes without conflicts
+  const int dpad = (a.d + 3) & ~3;
   float* kv = smem;                                // [kTile][pitch] values without their scale
-  float* qs = kv + kTile * pitch;                  // [kBlockCols][d]
-  float* tsc = qs + kBlockCols * a.d;              // [kTile] scale
-  int* tt = reinterpret_cast<int*>(tsc + kTile);   // [kTile] token (or -1), bit 31 set for list entries
-  long long* trow = reinterpret_cast<long long*>(tt + kTile);   // [kTile] row (8-byte aligned: kTile and kBlockCols are even)
+  float* qs = kv + kTile * pitch;                  // [kWarps][dpad]
+  float* ps = qs + kWarps * dpad;                  // [kWarps][kTile] weights times scales
+  float* tsc = ps + kWarps * kTile;                // [kTile] scale
+  uint32_t* tt = reinterpret_cast<uint32_t*>(tsc + kTile);   // [kTile] token, ~0 for none, bit 31 set for list entries
+  long long* trow = reinterpret_cast<long long*>(tt + kTile);   // [kTile] row
   const int hg = a.H / g.G, ncol = a.Tq * hg;
-  long long u = blockIdx.x;
+  uint32_t u = blockIdx.x;
   const int part = static_cast<int>(u % a.splits); u /= a.splits;
   const int cb = static_cast<int>(u % col_blocks); u /= col_blocks;
   const int head = static_cast<int>(u % g.G), b = static_cast<int>(u / g.G);
@@ -47,29 +50,23 @@ kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
   const int tiles = (sp.total + kTile - 1) / kTile;
   const int tile0 = static_cast<int>(static_cast<long long>(tiles) * part / a.splits);
   const int tile1 = static_cast<int>(static_cast<long long>(tiles) * (part + 1) / a.splits);
-
-  for (int e = threadIdx.x; e < kBlockCols * a.d; e += blockDim.x) {
-    const int c = cb * kBlockCols + e / a.d;
-    float v = 0.f;
-    if (c < ncol) {
-      const size_t at = ((static_cast<size_t>(b) * a.Tq + c / hg) * a.H + head * hg + c % hg) * a.d + e % a.d;
-      v = a.qdt == LSA_F32 ? static_cast<const float*>(a.q)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at]);
+  const int col = cb * kWarps + warp, cc = min(col, ncol - 1), qi = cc / hg;
+  {
+    const size_t at = ((static_cast<size_t>(b) * a.Tq + qi) * a.H + head * hg + (cc - qi * hg)) * a.d;
+    for (int e = lane; e < dpad; e += 32) {
+      float v = 0.f;
+      if (e < a.d) v = a.qdt == LSA_F32 ? static_cast<const float*>(a.q)[at + e] : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[at + e]);
+      qs[warp * dpad + e] = v;
     }
-    qs[e] = v;
   }
-  const int vpl = (a.dv + 31) / 32;
-  float acc[kCols][kMaxVpl], m[kCols], l[kCols];
-  int pos[kCols];
+  float acc[kMaxVpl], m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    m[c] = -INFINITY;
-    l[c] = 0.f;
-    const int col = cb * kBlockCols + warp * kCols + c;
-    pos[c] = sp.len - a.Tq + min(col, ncol - 1) / hg;
-#pragma unroll
-    for (int k = 0; k < kMaxVpl; ++k) acc[c][k] = 0.f;
-  }
+  for (int k = 0; k < kMaxVpl; ++k) acc[k] = 0.f;
+  // value column of accumulator k, in steps of four with kVec
+  auto vcol = [&](int k) { return kVec ? (k >> 2) * 128 + lane * 4 + (k & 3) : lane + 32 * k; };
+  const int pos = sp.len - a.Tq + qi;
   const float xs = a.sm * 1.44269504088896f;       // log2 e
+  const int wpr = rows_used / 4;                   // 4-code words of a row
   for (int tile = tile0; tile < tile1; ++tile) {
     __syncthreads();
     if (threadIdx.x < kTile) {
@@ -89,90 +86,95 @@ kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
       }
       tsc[threadIdx.x] = s;
       trow[threadIdx.x] = row;
-      tt[threadIdx.x] = t < 0 ? -1 : main ? t : static_cast<int>(0x80000000u | static_cast<uint32_t>(t));
+      tt[threadIdx.x] = t < 0 ? 0xffffffffu : main ? static_cast<uint32_t>(t) : 0x80000000u | static_cast<uint32_t>(t);
     }
     __syncthreads();
-    const int vpr = rows_used / 16;
-    for (int i = threadIdx.x; i < kTile * vpr; i += blockDim.x) {
-      const int t = i / vpr, v = i - t * vpr;
+    for (int t = warp; t < kTile; t += kWarps) {   // a warp a row
       const long long row = trow[t];
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (row >= 0) c = __ldg(reinterpret_cast<const uint4*>(g.rows + (static_cast<size_t>(row) * g.G + head) * g.W) + v);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      float* dst = kv + t * pitch + v * 16;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) dst[k] = e4m3_to_float(static_cast<uint8_t>(w[k / 4] >> (8 * (k % 4))));
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(g.rows + (static_cast<size_t>(row < 0 ? 0 : row) * g.G + head) * g.W);
+#pragma unroll 4
+      for (int i = lane; i < wpr; i += 32) {
+        const uint32_t c = row >= 0 ? __ldg(src + i) : 0u;
+        const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
+        const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3)));
+        *reinterpret_cast<float4*>(kv + t * pitch + 4 * i) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
     __syncthreads();
-    const uint32_t tok = static_cast<uint32_t>(tt[lane]);
+    const uint32_t tok = tt[lane];
     const float s = tsc[lane];
-    float x[kCols];
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) x[c] = 0.f;
-    const float* kr = kv + lane * pitch;
-    const float* q0 = qs + warp * kCols * a.d;
-    for (int k = 0; k < a.d; ++k) {
-      const float kvv = kr[k];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) x[c] = fmaf(q0[c * a.d + k], kvv, x[c]);
+    float4 x4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* kr = reinterpret_cast<const float4*>(kv + lane * pitch);
+    const float4* qr = reinterpret_cast<const float4*>(qs + warp * dpad);
+#pragma unroll 4
+    for (int k = 0; k < dpad / 4; ++k) {
+      const float4 kk = kr[k], q = qr[k];
+      x4.x = fmaf(q.x, kk.x, x4.x);
+      x4.y = fmaf(q.y, kk.y, x4.y);
+      x4.z = fmaf(q.z, kk.z, x4.z);
+      x4.w = fmaf(q.w, kk.w, x4.w);
     }
+    bool see = tok != 0xffffffffu;
+    if (see) {
+      const bool in_main = kv_sees(a, static_cast<int>(tok & 0x7fffffffu), pos);
+      see = (tok >> 31) ? !in_main : in_main;
+    }
+    const float x = see ? ((x4.x + x4.y) + (x4.z + x4.w)) * (xs * s) : -INFINITY;
+    float tm = x;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      bool see = tok != 0xffffffffu;
-      if (see) {
-        const int t = static_cast<int>(tok & 0x7fffffffu);
-        const bool in_main = kv_sees(a, t, pos[c]);
-        see = (tok >> 31) ? !in_main : in_main;
-      }
-      x[c] = see ? x[c] * (xs * s) : -INFINITY;
-      float tm = x[c];
-      bool bad = see && !(s <= 3.4e38f);             // a block marked non-finite makes the result NaN
+    for (int o = 16; o > 0; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+    const float mn = fmaxf(m, tm);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m - ref);                // 0 while nothing has been seen
+    float p = see ? exp2f(x - ref) : 0.f;
+    if (see && !(s <= 3.4e38f)) p = __int_as_float(0x7fc00000);   // a block marked non-finite makes the result NaN
+    m = mn;
+    float sum = p;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
-      const float mn = fmaxf(m[c], tm);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m[c] - ref);             // 0 while nothing has been seen
-      float p = see ? exp2f(x[c] - ref) : 0.f;
-      if (bad) p = __int_as_float(0x7fc00000);
-      m[c] = mn;
-      float ps = p;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * f + sum;
+    ps[warp * kTile + lane] = see ? p * s : 0.f;
+    __syncwarp();
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-      l[c] = l[c] * f + ps;
-      const float pv = see ? p * s : 0.f;
+    for (int k = 0; k < kMaxVpl; ++k) acc[k] *= f;
+#pragma unroll 2
+    for (int t = 0; t < kTile; ++t) {
+      const float w = ps[warp * kTile + t];
+      const float* vr = kv + t * pitch + a.voff;
+      if constexpr (kVec) {
 #pragma unroll
-      for (int k = 0; k < kMaxVpl; ++k) acc[c][k] *= f;
-      for (int t = 0; t < kTile; ++t) {
-        const float w = __shfl_sync(0xffffffffu, pv, t);
-        const float* vr = kv + t * pitch + a.voff + lane;
+        for (int k = 0; k < kMaxVpl; k += 4)
+          if (vcol(k) < a.dv) {
+            const float4 v = *reinterpret_cast<const float4*>(vr + vcol(k));
+            acc[k] = fmaf(w, v.x, acc[k]);
+            acc[k + 1] = fmaf(w, v.y, acc[k + 1]);
+            acc[k + 2] = fmaf(w, v.z, acc[k + 2]);
+            acc[k + 3] = fmaf(w, v.w, acc[k + 3]);
+          }
+      } else {
 #pragma unroll
         for (int k = 0; k < kMaxVpl; ++k)
-          if (k < vpl && lane + 32 * k < a.dv) acc[c][k] = fmaf(w, vr[32 * k], acc[c][k]);
+          if (vcol(k) < a.dv) acc[k] = fmaf(w, vr[vcol(k)], acc[k]);
       }
     }
   }
+  if (col >= ncol) return;
+  if (a.splits > 1) {
+    const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + part) * ncol + col;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    const int col = cb * kBlockCols + warp * kCols + c;
-    if (col >= ncol) continue;
-    if (a.splits > 1) {
-      const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + part) * ncol + col;
-#pragma unroll
-      for (int k = 0; k < kMaxVpl; ++k)
-        if (k < vpl && lane + 32 * k < a.dv) a.part_o[pc * a.dv + lane + 32 * k] = acc[c][k];
-      if (lane == 0) {
-        a.part_m[pc] = m[c];
-        a.part_l[pc] = l[c];
-      }
-    } else {
-      const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
-      const float r = l[c] == 0.f ? 0.f : 1.0f / l[c];
-#pragma unroll
-      for (int k = 0; k < kMaxVpl; ++k)
-        if (k < vpl && lane + 32 * k < a.dv) store_out(a.out, a.qdt, oc * a.dv + lane + 32 * k, acc[c][k] * r);
-      if (lane == 0 && a.lse != nullptr)
-        a.lse[oc] = l[c] == 0.f ? -INFINITY : (m[c] + log2f(l[c])) * 0.693147180559945f;
+    for (int k = 0; k < kMaxVpl; ++k)
+      if (vcol(k) < a.dv) a.part_o[pc * a.dv + vcol(k)] = acc[k];
+    if (lane == 0) {
+      a.part_m[pc] = m;
+      a.part_l[pc] = l;
     }
+  } else {
+    const size_t oc = (static_cast<size_t>(b) * a.Tq + qi) * a.H + head * hg + (cc - qi * hg);
+    const float r = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+    for (int k = 0; k < kMaxVpl; ++k)
+      if (vcol(k) < a.dv) store_out(a.out, a.qdt, oc * a.dv + vcol(k), acc[k] * r);
+    if (lane == 0 && a.lse != nullptr) a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
   }
 }
 
@@ -248,28 +250,28 @@ __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendAr
 }
 
 size_t simt_smem(const KvAttendArgs& a, int rows_used) {
-  const int pitch = rows_used | 1;
-  return static_cast<size_t>(kTile * pitch + kBlockCols * a.d + 2 * kTile + 2) * 4 + kTile * 8;
+  const int pitch = (rows_used + 31) / 32 * 32 + 4, dpad = (a.d + 3) & ~3;
+  return static_cast<size_t>(kTile * pitch + kWarps * dpad + kWarps * kTile + 2 * kTile) * 4 + kTile * 8;
 }
 
 }  // namespace
 
 int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens) {
-  const long long units = static_cast<long long>(B) * G * ((ncol + kBlockCols - 1) / kBlockCols);
+  const long long units = static_cast<long long>(B) * G * ((ncol + kWarps - 1) / kWarps);
   const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
-  // About four blocks per SM, at least two tiles in a part.
-  return static_cast<int>(std::max<long long>(1, std::min<long long>({(4 * 148 + units - 1) / units, (tiles + 1) / 2, 256})));
+  // Up to four blocks per SM, and eight tiles in a part: a shorter one costs less than the join.
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({(4 * 148 + units - 1) / units, (tiles + 7) / 8, 256})));
 }
 
 int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s) {
-  const int ncol = a.Tq * (a.H / a.g.G), col_blocks = (ncol + kBlockCols - 1) / kBlockCols;
+  const int ncol = a.Tq * (a.H / a.g.G), col_blocks = (ncol + kWarps - 1) / kWarps;
   const int rows_used = (std::max(a.d, a.voff + a.dv) + 15) / 16 * 16;
   const size_t smem = simt_smem(a, rows_used);
-  const cudaError_t e = cudaFuncSetAttribute(kv_attend_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  const auto kern = a.voff % 4 == 0 && a.dv % 4 == 0 ? kv_attend_simt_kernel<true> : kv_attend_simt_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
   const long long grid = static_cast<long long>(a.g.B) * a.g.G * col_blocks * a.splits;
-  kv_attend_simt_kernel<<<static_cast<unsigned>(grid), kWarps * 32, smem, s>>>(a, col_blocks, rows_used);
+  kern<<<static_cast<unsigned>(grid), kWarps * 32, smem, s>>>(a, col_blocks, rows_used);
   return check_launch("kv_attend");
 }
 
