@@ -223,9 +223,6 @@ __device__ __forceinline__ float warp_max(float x) {               // NaN is ign
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // Arrives at the barrier when this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -338,6 +335,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     u = q;
     return static_cast<int>(r);
   };
+  pdl_wait();                                              // what follows reads the call's inputs
   const int rank = digit(t.cluster), cg = digit(t.col_groups), grp = digit(a.splits), head = digit(g.G);   // a.splits: clusters of a unit
   const int b = static_cast<int>(u);
   const int c_base = cg * C, n_c = min(C, ncol - c_base);
@@ -389,6 +387,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     const int n_kf = pl.n_k - pl.tail, gap = max(pl.v0 - n_kf, 0);   // chunks between keys and values are not read
     const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
     const uint64_t policy = normal_policy();
+    const int v_slot0 = plan_v_slot(pl, pl.v0);
     const int piece = lane & 7, r_in = lane >> 3;          // a lane's 16 bytes of a chunk and its row of four
     const uint8_t* lane_base = g.rows + static_cast<size_t>(head) * g.W + piece * 16;
     // A token takes three dependent loads (list, table, scale beside the row): each is issued
@@ -446,70 +445,81 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       // whether the warp's rows are runs of t.run rows, for the TMA
       const int in_run = t.run > 0 ? lane & (t.run - 1) : 0, run_first = __shfl_sync(0xffffffffu, row, lane - in_run);
       const bool runs = __all_sync(0xffffffffu, t.run > 0 && row >= 0 && row == run_first + in_run);
-      // This lane's rows of the copies, four rows an instruction, and whether all are there.
-      const uint8_t* src[8];
-      uint32_t there = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = __shfl_sync(0xffffffffu, row, k * 4 + (lane >> 3));
-        there |= (r >= 0 ? 1u : 0u) << k;
-        src[k] = lane_base + static_cast<size_t>(max(r, 0)) * row_bytes;
-      }
-      const bool whole = __all_sync(0xffffffffu, there == 0xffu);
-      const int row0 = __shfl_sync(0xffffffffu, row, 0), row16 = __shfl_sync(0xffffffffu, row, 16);
-      // The chunks in order, the tail before the last of them: its slot is free earlier.
-      for (int step = 0; step < pl.n_full + pl.tail && ok; ++step) {
-        const bool is_tail = pl.tail && step == pl.n_full - 1;
-        const int c = pl.tail && step == pl.n_full ? step - 1 : step;
-        const int slot = s * pl.n_full + c, col = (c < n_kf || is_tail ? (is_tail ? n_kf : c) : c + gap) * 128;
-        uint64_t* full_bar = is_tail ? &tfull[ts] : &full[slot];
-        ok = __all_sync(0xffffffffu, is_tail ? mbar_wait(&tempty[ts], tph ^ 1, abort_flag) : mbar_wait(&empty[slot], ph ^ 1, abort_flag));
-        if (!ok) break;
-        const uint32_t width = is_tail ? 64 : 128;
-        uint8_t* const to = (is_tail ? tails + ts * kTailBytes : ring + static_cast<size_t>(slot) * kChunkBytes) + warp * 32 * width;
-        if (runs) {
-          if (lane == 0) {
-            expect_bytes(full_bar, 32 * width);
-            if (is_tail) {
-              tma_load_3d(to, &map_tail, col, head, row0, full_bar, policy);
-              if (t.run == 16) tma_load_3d(to + 16 * 64, &map_tail, col, head, row16, full_bar, policy);
-            } else {
-              tma_load_3d(to, &map, col, head, row0, full_bar, policy);
-              if (t.run == 16) tma_load_3d(to + 16 * 128, &map, col, head, row16, full_bar, policy);
-            }
+      // The stage's token words are free once the values of its last tile have begun.  When all
+      // rows are runs they carry the runs' first rows to the warps, each of which brings whole
+      // chunks as their slots become free; else a warp brings its 32 rows, chunk by chunk.
+      if (ok) ok = mbar_wait(&empty[s * pl.n_full + v_slot0], ph ^ 1, abort_flag);
+      float2* words = info + s * kTile;
+      words[threadIdx.x].x = __int_as_float(row);
+      if (!group_any(6, !runs || !ok)) {
+        // The others' chunks get nothing from this warp (their slots' last phase is over: the stage's
+        // values have begun).
+        for (int c = 0; c < pl.n_full; ++c)
+          if ((c & 3) != warp) mbar_arrive(&full[s * pl.n_full + c]);
+        for (int c = warp; c < pl.n_full + pl.tail; c += 4) {
+          const bool is_tail = c == pl.n_full;
+          const int slot = s * pl.n_full + c, col = (is_tail ? n_kf : c < n_kf ? c : c + gap) * 128;
+          uint64_t* full_bar = is_tail ? &tfull[ts] : &full[slot];
+          if (!__all_sync(0xffffffffu, mbar_wait(is_tail ? &tempty[ts] : &empty[slot], (is_tail ? tph : ph) ^ 1, abort_flag))) {
+            ok = false;
+            break;
           }
+          if (lane == 0) expect_bytes(full_bar, is_tail ? kTailBytes : kChunkBytes);
           __syncwarp();
           mbar_arrive(full_bar);
-        } else if (!is_tail) {
-          const bool in = col + piece * 16 < g.W;          // past the row's end there is nothing to read
-          const uint32_t at0 = smem_u32(to) + r_in * 128 + ((piece ^ r_in) * 16), at1 = at0 ^ 64;
-          if (whole && col + 128 <= g.W) {
+          if (lane < kTile / t.run) {                      // a lane a box
+            const int r = lane * t.run, row0 = __float_as_int(words[r].x);
+            if (is_tail) tma_load_3d(tails + ts * kTailBytes + r * 64, &map_tail, col, head, row0, full_bar, policy);
+            else tma_load_3d(ring + static_cast<size_t>(slot) * kChunkBytes + r * 128, &map, col, head, row0, full_bar, policy);
+          }
+        }
+        __syncwarp();
+        if (pl.tail && (pl.n_full & 3) != warp) {          // one tail may serve all stages: its last phase must be over
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&tempty[ts], tph ^ 1, abort_flag));
+          if (ok) mbar_arrive(&tfull[ts]);
+        }
+        if (group_any(6, !ok)) break;                      // (and every warp has read the rows)
+      } else {
+        if (group_any(6, !ok)) break;                      // the same for the four warps
+        const uint8_t* src[8];                             // this lane's rows of the copies, four rows an instruction
+        uint32_t there = 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) copy16(((k & 1) ? at1 : at0) + k * 512, src[k] + col);
-          } else {
+        for (int k = 0; k < 8; ++k) {
+          const int r = __shfl_sync(0xffffffffu, row, k * 4 + r_in);
+          there |= (r >= 0 ? 1u : 0u) << k;
+          src[k] = lane_base + static_cast<size_t>(max(r, 0)) * row_bytes;
+        }
+        // the tail before the last chunk: its slot is free earlier
+        for (int step = 0; step < pl.n_full + pl.tail; ++step) {
+          const bool is_tail = pl.tail && step == pl.n_full - 1;
+          const int c = pl.tail && step == pl.n_full ? step - 1 : step;
+          const int slot = s * pl.n_full + c, col = (is_tail ? n_kf : c < n_kf ? c : c + gap) * 128;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(is_tail ? &tempty[ts] : &empty[slot], (is_tail ? tph : ph) ^ 1, abort_flag));
+          if (!ok) continue;
+          if (!is_tail) {
+            const bool in = col + piece * 16 < g.W;        // past the row's end there is nothing to read
+            const uint32_t at0 = smem_u32(ring) + slot * kChunkBytes + warp * 4096 + r_in * 128 + ((piece ^ r_in) * 16), at1 = at0 ^ 64;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const bool real = in && ((there >> k) & 1);
               copy16(((k & 1) ? at1 : at0) + k * 512, src[k] + (in ? col : 0), real ? 16u : 0u);
             }
-          }
-          copies_arrive(full_bar);
-        } else {
-          const int p4 = lane & 3, r8 = lane >> 2;         // eight rows an instruction
-          const bool in = col + p4 * 16 < g.W;
-          const uint8_t* base = g.rows + static_cast<size_t>(head) * g.W + (in ? col + p4 * 16 : 0);
-          const uint32_t at = smem_u32(to) + r8 * 64 + ((p4 ^ ((r8 >> 1) & 3)) * 16);
+            copies_arrive(&full[slot]);
+          } else {
+            const int p4 = lane & 3, r8 = lane >> 2;       // eight rows an instruction
+            const bool in = col + p4 * 16 < g.W;
+            const uint8_t* base = g.rows + static_cast<size_t>(head) * g.W + (in ? col + p4 * 16 : 0);
+            const uint32_t at = smem_u32(tails) + ts * kTailBytes + warp * 2048 + r8 * 64 + ((p4 ^ ((r8 >> 1) & 3)) * 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = __shfl_sync(0xffffffffu, row, k * 8 + r8);
-            copy16(at + k * 512, base + static_cast<size_t>(max(r, 0)) * row_bytes, r >= 0 && in ? 16u : 0u);
+            for (int k = 0; k < 4; ++k) {
+              const int r = __shfl_sync(0xffffffffu, row, k * 8 + r8);
+              copy16(at + k * 512, base + static_cast<size_t>(max(r, 0)) * row_bytes, r >= 0 && in ? 16u : 0u);
+            }
+            copies_arrive(&tfull[ts]);
           }
-          copies_arrive(full_bar);
         }
       }
-      if (!ok) break;
-      // every slot was free, so the weights of the stage's last tile have been read
-      info[s * kTile + threadIdx.x] = make_float2(scale, __int_as_float(word));
+      words[threadIdx.x] = make_float2(scale, __int_as_float(word));
       mbar_arrive(&ifull[s]);
       if (++s == pl.stages) { s = 0; ph ^= 1; }
       if (++ts == pl.tstages) { ts = 0; tph ^= 1; }
@@ -883,6 +893,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
     }
   }
+  pdl_trigger();
   tc_fence_before();
   if (t.cluster > 1) cluster_sync();
   else __syncthreads();
@@ -1018,7 +1029,9 @@ int launch_c(const CUtensorMap& map, const CUtensorMap& tail, const AttendTc& t,
   const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, t.p.smem);
   if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = t.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -1027,7 +1040,7 @@ int launch_c(const CUtensorMap& map, const CUtensorMap& tail, const AttendTc& t,
   cfg.dynamicSmemBytes = t.p.smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   cudaLaunchKernelEx(&cfg, kv_attend_tc_kernel<C>, map, tail, t);
   return check_launch("kv_attend");
 }
