@@ -178,16 +178,19 @@ kv_attend_simt_kernel(const KvAttendArgs a, int col_blocks, int rows_used) {
   }
 }
 
-// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a column's parts: a block a column,
-// the parts' weights first (a thread a part), then four columns a thread.
-__global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendArgs a) {
+// out = sum_p 2^(m_p - m) o_p / sum_p 2^(m_p - m) l_p over a column's parts: a block for a
+// column and 128 of its values.  The parts' weights come first (a thread a part), then each
+// of the four warps sums every fourth part, four values a lane.
+__global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendArgs a, int slices) {
   __shared__ float wt[256];
   __shared__ float red[8];
+  __shared__ float4 sums[4][32];
   pdl_wait();
   const KvGeom& g = a.g;
   const int hg = a.H / g.G, ncol = a.Tq * hg;
-  const long long u = blockIdx.x / ncol;
-  const int col = static_cast<int>(blockIdx.x % ncol);
+  const uint32_t cu = blockIdx.x / slices, slice = blockIdx.x - cu * slices;
+  const uint32_t u = cu / ncol;
+  const int col = static_cast<int>(cu - u * ncol);
   const int head = static_cast<int>(u % g.G), b = static_cast<int>(u / g.G);
   const size_t base = static_cast<size_t>(u) * a.splits * ncol + col;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendAr
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const float w = pl[k] != 0.f ? exp2f(pm[k] - m) : 0.f;
-    if (threadIdx.x + 128 * k < 256) wt[threadIdx.x + 128 * k] = w;
+    wt[threadIdx.x + 128 * k] = w;
     l += pl[k] != 0.f ? w * pl[k] : 0.f;
   }
 #pragma unroll
@@ -217,36 +220,56 @@ __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendAr
   if (lane == 0) red[4 + warp] = l;
   __syncthreads();
   l = (red[4] + red[5]) + (red[6] + red[7]);
-  const size_t oc = (static_cast<size_t>(b) * a.Tq + col / hg) * a.H + head * hg + col % hg;
+  const int qi = a.Tq == 1 ? 0 : col / hg;
+  const size_t oc = (static_cast<size_t>(b) * a.Tq + qi) * a.H + head * hg + (col - qi * hg);
   const float r = l == 0.f ? 0.f : 1.0f / l;
   const float* po = a.part_o + base * a.dv;
   const size_t step = static_cast<size_t>(ncol) * a.dv;
+  const int v = slice * 128 + lane * 4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.dv % 4 == 0) {
-    for (int k = threadIdx.x; k < a.dv / 4; k += 128) {
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
+    if (v < a.dv) {
 #pragma unroll 8
-      for (int p = 0; p < a.splits; ++p) {
-        const float4 v = *reinterpret_cast<const float4*>(po + p * step + 4 * k);
+      for (int p = warp; p < a.splits; p += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(po + p * step + v);
         const float w = wt[p];
         if (w != 0.f) {                                    // a part without tokens has stored nothing
-          o[0] = fmaf(w, v.x, o[0]);
-          o[1] = fmaf(w, v.y, o[1]);
-          o[2] = fmaf(w, v.z, o[2]);
-          o[3] = fmaf(w, v.w, o[3]);
+          o.x = fmaf(w, f.x, o.x);
+          o.y = fmaf(w, f.y, o.y);
+          o.z = fmaf(w, f.z, o.z);
+          o.w = fmaf(w, f.w, o.w);
         }
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) store_out(a.out, a.qdt, oc * a.dv + 4 * k + e, o[e] * r);
     }
   } else {
-    for (int k = threadIdx.x; k < a.dv; k += 128) {
-      float o = 0.f;
-      for (int p = 0; p < a.splits; ++p)
-        if (wt[p] != 0.f) o = fmaf(wt[p], po[p * step + k], o);
-      store_out(a.out, a.qdt, oc * a.dv + k, o * r);
+    for (int p = warp; p < a.splits; p += 4) {
+      const float w = wt[p];
+      if (w == 0.f) continue;
+      const float* f = po + p * step;
+      if (v < a.dv) o.x = fmaf(w, f[v], o.x);
+      if (v + 1 < a.dv) o.y = fmaf(w, f[v + 1], o.y);
+      if (v + 2 < a.dv) o.z = fmaf(w, f[v + 2], o.z);
+      if (v + 3 < a.dv) o.w = fmaf(w, f[v + 3], o.w);
     }
   }
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+  sums[warp][lane] = o;
+  __syncthreads();
+  if (warp == 0) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 f = sums[k][lane];
+      s[0] += f.x;
+      s[1] += f.y;
+      s[2] += f.z;
+      s[3] += f.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (v + e < a.dv) store_out(a.out, a.qdt, oc * a.dv + v + e, s[e] * r);
+  }
+  if (threadIdx.x == 0 && slice == 0 && a.lse != nullptr)
+    a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
 }
 
 size_t simt_smem(const KvAttendArgs& a, int rows_used) {
@@ -276,8 +299,9 @@ int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s) {
 }
 
 int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s) {
-  const long long grid = static_cast<long long>(a.g.B) * a.g.G * a.Tq * (a.H / a.g.G);
-  const cudaError_t e = launch_dependent(kv_attend_combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(128), 0, s, a);
+  const int slices = (a.dv + 127) / 128;
+  const long long grid = static_cast<long long>(a.g.B) * a.g.G * a.Tq * (a.H / a.g.G) * slices;   // at most 2^26
+  const cudaError_t e = launch_dependent(kv_attend_combine_kernel, dim3(static_cast<unsigned>(grid)), dim3(128), 0, s, a, slices);
   if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
   return check_launch("kv_attend_combine");
 }
