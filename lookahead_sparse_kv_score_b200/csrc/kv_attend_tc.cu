@@ -111,7 +111,8 @@ Plan make_plan(int d, int dv, int voff, int C, int limit) {
   p.ksteps = (d + 31) / 32;
   const int q_bytes = 2 * C * (n_kf * 128 + p.tail * 64);     // a multiple of 1024
   const int stage = p.n_full * kChunkBytes;
-  const int fixed = q_bytes + kChunkBytes /* weights */ + kBars * 8 + C * (8 + 2);
+  const int p_bytes = 2 * kTile * C;                           // weights, first and second terms
+  const int fixed = q_bytes + p_bytes + kBars * 8 + C * (8 + 2);
   // whole stages with their tails while they fit, else two stages on one tail
   const int per = stage + p.tail * kTailBytes + kTile * 8;
   p.stages = std::min({kMaxStages, (limit - fixed) / per, kMaxSlots / p.n_full});
@@ -122,7 +123,7 @@ Plan make_plan(int d, int dv, int voff, int C, int limit) {
   }
   p.q_off = p.stages * stage;
   p.p_off = p.q_off + q_bytes;
-  p.t_off = p.p_off + kChunkBytes;
+  p.t_off = p.p_off + p_bytes;
   p.i_off = p.t_off + p.tail * p.tstages * kTailBytes;
   p.m_off = p.i_off + p.stages * kTile * 8;
   p.smem = p.m_off + kBars * 8 + C * (8 + 2);
@@ -142,6 +143,10 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t group, uint32_t swizzle) {
   return (group >> 4) | (1u << 14) | (swizzle << 29);
 }
+// The weights are not swizzled: blocks of 16 columns, [128 tokens][16 bytes] each.  Eight tokens
+// (128 bytes) are a core matrix; the leading offset goes to the next eight, the stride to the
+// next 16 columns.
+__device__ __forceinline__ uint32_t desc_p_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | ((128u >> 4) << 16); }
 
 // kind::f8f6f4, fp32 accumulators, M = 128: operand types (0 e4m3, 1 e5m2), both operands
 // K-major (mn = 0) or both MN-major (mn = 1).
@@ -608,7 +613,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         if (++ts == pl.tstages) { ts = 0; tph ^= 1; }
       }
     } else {
-      const uint32_t bd = uniform(desc_lo(smem_u32(pbuf)));
+      const uint32_t bd = uniform(desc_p_lo(smem_u32(pbuf)));
+      constexpr uint32_t kHiP = desc_hi(2048, 0);
       int s = 0;
       uint32_t ph = 0;
       for (int j = 0; ok && j < n; ++j) {
@@ -625,8 +631,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
           if (elect()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 256, kHi128, id_hi, ks > 0 ? 1u : acc);
-              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 256 + 4, kHi128, id_lo, 1u);
+              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 32, kHiP, id_hi, ks > 0 ? 1u : acc);
+              mma_lo(d_t, ad + ks * 256, kHi128, bd + ks * 32 + (C / 16) * 128, kHiP, id_lo, 1u);
             }
             mma_commit(&empty[slot]);
             if (m + 1 == n_v) mma_commit(pdone);
@@ -723,12 +729,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       if (lane == 0) mbar_arrive(qfull);
       asm volatile("barrier.cta.sync 5, %0;" ::"n"(32 * Sh::kWeights) : "memory");   // the columns' factors, to all
     }
-    // Scratch of 256 words for the group, in its own columns' bytes of the weights buffer (two
-    // words a row), while no MMA reads them.
-    auto scratch = [&](int i) {
-      const int r = i >> 1;
-      return reinterpret_cast<float*>(pbuf + r * 128 + (((c0 >> 4) ^ (r & 7)) * 16) + (c0 & 15) + (i & 1) * 4);
-    };
+    // Scratch of 512 words for the group, in its own columns' block of the weights buffer, while no
+    // MMA reads it.
+    auto scratch = [&](int i) { return reinterpret_cast<float*>(pbuf + wg * 2048) + i; };
     float2 l[NC / 2];
 #pragma unroll
     for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
@@ -864,13 +867,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         lw[c / 4] = l0 | (l1 << 16);
       }
       if (ok && j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
-      uint8_t* pr = pbuf + row * 128;
-#pragma unroll
-      for (int k = 0; k < NC / 16; ++k) {
-        const int ch = c0 / 16 + k, cl = 4 + ch;
-        *reinterpret_cast<uint4*>(pr + ((ch ^ (row & 7)) * 16)) = make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]);
-        *reinterpret_cast<uint4*>(pr + ((cl ^ (row & 7)) * 16)) = make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]);
-      }
+      uint8_t* pr = pbuf + wg * 2048 + row * 16;
+      *reinterpret_cast<uint4*>(pr) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(pr + (C / 16) * 2048) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_fence_before();
       __syncwarp();
@@ -1104,7 +1103,7 @@ void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long lo
       double c = blocks <= slots[k] ? w * (per_sm > 1.0 ? 1.5 : 1.0)
                  : blocks <= room ? w * 2.2
                                   : per_sm * w * (per_sm > 1.0 ? blocks / room + 0.25 : std::ceil(blocks / room));
-      c += (gr > 1 ? 3.0 + gr / 16.0 : 0.0) + 0.25 * k;
+      c += (gr > 1 ? (3.0 + gr / 16.0) * (per_sm > 1.0 ? 3.0 : 1.0) : 0.0) + 0.25 * k;
       if (best < 0.0 || c < best) {
         best = c;
         cluster = static_cast<int>(X);
