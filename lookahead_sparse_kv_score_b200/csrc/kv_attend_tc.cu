@@ -14,10 +14,12 @@
 // 448, an e4m3 term holds the first four and a second one the rest, exactly, except
 // below 2^-10 / 224 of the row's largest element.  A weight P'' (see below) is held as an e4m3
 // and an e5m2 term: half a step of each is 2^-4 * 2^-3 = 2^-7 of the weight at most (rms
-// 1.2e-3, below the bf16 rounding of the result), and the e5m2 range keeps weights down to
-// 2^-17.  The reference weight is 2^k with k = log2(tokens of the part) - 8 (0 to 6, parts
-// of at most 16384 tokens), so the weights lost below the range are less than 2^-9 of the sum.
-// Scores, the sum of the weights and the accumulators are fp32.
+// 1.2e-3, below the bf16 rounding of the result); below 2^-6 of the unit the first term's steps
+// stop shrinking and the error is 2^-13 of the unit or an eighth of the weight, whichever is
+// less, and the e5m2 range keeps weights down to 2^-17.  The reference weight is 2^k units with
+// k = log2(tokens of the part) - 8 (0 to 6, parts of at most 16384 tokens), so the weights
+// lost below the range are less than 2^-9 of the sum.  Scores, the sum of the weights and the
+// accumulators are fp32.
 //
 // Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2(scale_t); the value weight is
 // P''_tc = 2^(y_tc - r_c) and the softmax weight P''_tc / scale_t, so one exponential serves

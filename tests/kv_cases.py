@@ -78,9 +78,11 @@ def tolerances(dtype, d, r, vmax):
     brings its row's largest element to (224, 448]: exact but for at most 2^-10 / 224 of that
     element where the second term is subnormal.
     Weights: e^(2 dx) - 1 (the token's own score and the sum's), the exponential (2^-21) and
-    the fp32 sums, (wide + 16) 2^-24.  The bf16 path multiplies values by a weight held as an
-    e4m3 plus an e5m2 term: off by at most half a step of each, 2^-4 * 2^-3, and by half the
-    smallest e5m2 value, 2^-17, where the largest weight is 64 or more.
+    the fp32 sums, (wide + 16) 2^-24.  The bf16 path multiplies the codes by a weight W = softmax *
+    scale held as an e4m3 plus an e5m2 term, in units where the largest of its part is at least
+    1: off by at most half a step of each, 2^-4 * 2^-3 of itself.  Below 2^-6 the first term's steps
+    are 2^-9, so what is left for the second is at most 2^-10 (and at most W) and its half step
+    2^-3 of that; and half the smallest e5m2 value is 2^-17 (below that all of W): r.lost.
     A weight below the smallest normal fp32 number may become 0: it is below 2^-126 of the
     largest weight, so the sum of values moves by at most wide 2^-126 vmax.
     The result is rounded once, by half a step (bf16 2^-8, fp32 2^-24)."""
@@ -91,7 +93,9 @@ def tolerances(dtype, d, r, vmax):
     if bf16:
         rel = rel + 2.0 ** -7
     out = rel[..., None] * r["mean"] + (2.0 ** -8 if bf16 else U32) * np.abs(r["out"])
-    out = out + ((2.0 ** -23 if bf16 else 2.0 ** -126) * vmax * r["wide"])[..., None]
+    out = out + (2.0 ** -126 * vmax * r["wide"])[..., None]
+    if bf16:
+        out = out + r["lost"]
     return out, lse
 
 
