@@ -1041,8 +1041,6 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
   if (t.cluster > 1) cluster_sync();                       // nobody reads this block's shared memory any more
 }
 
-int columns(int ncol) { return ncol <= 16 ? 16 : ncol <= 32 ? 32 : 64; }
-
 // Two blocks share an SM where each gets two stages of its half; one block has it all otherwise.
 Plan plan_for(int d, int dv, int voff, int C) {
   if (C < 64) {
@@ -1075,15 +1073,24 @@ int launch_c(const CUtensorMap& map, const CUtensorMap& tail, const AttendTc& t,
 
 }  // namespace
 
-bool kv_attend_tc_supported(long long max_tokens, int d, int dv, int voff, int qdt, int ncol) {
-  // 16384 tokens a part, at most 8 parts a cluster and 256 clusters a unit; tokens below 2^30
-  if (qdt != LSA_BF16 || d % 8 != 0 || d > 576 || max_tokens > 16384ll * 8 * 256) return false;
-  const Plan p = plan_for(d, dv, voff, columns(ncol));
-  return p.n_v <= 4 && p.stages >= 2 && p.smem <= kSmemLimit;
+int kv_attend_columns_tc(int B, int G, int ncol, long long max_tokens, int d, int dv, int voff, int qdt) {
+  // 16384 tokens a part, at most 8 parts a cluster and 256 clusters a unit
+  if (qdt != LSA_BF16 || d % 8 != 0 || d > 576 || max_tokens > 16384ll * 8 * 256) return 0;
+  // The columns a block can hold; fewer where the blocks would leave SMs idle all the same: a
+  // quarter of the columns is a quarter of the sums to join (512 rows, one sequence, 64 heads:
+  // 19.7 us with 64 columns a block).
+  const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
+  for (int C = 16; C <= 64; C *= 2) {
+    const bool enough = ncol <= C || C == 64;
+    if (!enough && static_cast<long long>(B) * G * ((ncol + C - 1) / C) * tiles > 148) continue;
+    const Plan p = plan_for(d, dv, voff, C);
+    if (p.n_v <= 4 && p.stages >= 2 && p.smem <= kSmemLimit) return C;
+    if (enough) return 0;
+  }
+  return 0;
 }
 
-void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups) {
-  const int C = columns(ncol);
+void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups) {
   const long long units = static_cast<long long>(B) * G * ((ncol + C - 1) / C);
   const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
   const long long least = (max_tokens + 16383) / 16384;   // parts, by the weights' range (see the top)
@@ -1116,8 +1123,8 @@ void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long lo
   }
 }
 
-int launch_kv_attend_tc(const KvAttendArgs& a, int cluster, cudaStream_t s) {
-  const int ncol = a.Tq * (a.H / a.g.G), C = columns(ncol);
+int launch_kv_attend_tc(const KvAttendArgs& a, int C, int cluster, cudaStream_t s) {
+  const int ncol = a.Tq * (a.H / a.g.G);
   AttendTc t{};
   t.a = a;
   t.p = plan_for(a.d, a.dv, a.voff, C);

@@ -102,10 +102,11 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
   return e < 0 ? -1 : e;
 }
 
-bool kv_attend_tc_supported(long long max_tokens, int d, int dv, int voff, int qdt, int ncol);
-// Blocks of a cluster and clusters of a unit (KvAttendArgs::splits) for the tensor-core path.
-void kv_attend_parts_tc(int B, int G, int ncol, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups);
-int launch_kv_attend_tc(const KvAttendArgs& a, int cluster, cudaStream_t s);
+// The tensor-core path: query columns of a block (16, 32 or 64; 0: shape not supported), blocks
+// of a cluster and clusters of a unit (KvAttendArgs::splits).
+int kv_attend_columns_tc(int B, int G, int ncol, long long max_tokens, int d, int dv, int voff, int qdt);
+void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups);
+int launch_kv_attend_tc(const KvAttendArgs& a, int C, int cluster, cudaStream_t s);
 int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens);
 int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s);
 int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s);
