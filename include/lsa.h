@@ -401,8 +401,10 @@ int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const i
  *   codes and scales must be finite (codes 0x7f and 0xff are not written by lsa_kv_write).
  *   d <= 576, dv <= 512, voff + dv <= 1024, H a multiple of G, B*Tq*H <= 2^24,
  *   Tq*H/G <= 65536, else LSA_ERR_UNSUPPORTED (or INVALID_ARG).
- * workspace: lsa_kv_attend_workspace_bytes(...) bytes, 256-byte aligned; calls that may
- *   overlap on the GPU need their own (calls captured into graphs that run at the same time too).
+ * One launch, or two (few sequences, long ones: the parts of a sequence are joined by the second).
+ * workspace: lsa_kv_attend_workspace_bytes(...) bytes for the same sizes (cap = 0 without a
+ *   list), 256-byte aligned; calls that may overlap on the GPU need their own, calls captured
+ *   into graphs that run at the same time among them.
  * ---------------------------------------------------------------------------------- */
 size_t lsa_kv_attend_workspace_bytes(int B, int Tq, int N, int H, int G, int d, int dv, int voff, int W, int qdt,
                                      int sinks, int window, int cap);

@@ -232,7 +232,9 @@ def _dev_strided(t, name, dtypes, span, device):
     view's first one must lie in its storage."""
     if t.dtype not in dtypes or t.get_device() != device or device < 0:
         raise ValueError(_bad(t, name, dtypes, 0, device))
-    if (t.storage_offset() + span) * t.element_size() > t.untyped_storage().nbytes():
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension has stride {t.stride(-1)}; it must be dense")
+    if span < 0 or (t.storage_offset() + span) * t.element_size() > t.untyped_storage().nbytes():
         raise ValueError(f"{name}: {span} elements from its first one lie outside its storage")
     return t.data_ptr()
 

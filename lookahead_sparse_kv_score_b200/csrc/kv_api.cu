@@ -157,7 +157,10 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
   KvGeom g{};
   int rc = make_geom("kv_attend", B, N, G, W, block, page, seq_pages, pages, table, rows, scale, g);
   if (rc != LSA_OK) return rc;
-  if (!idx) cap = 0;
+  if (!idx || N == 0) {   // no list, or none of its entries can be a token
+    idx = nullptr;
+    cap = 0;
+  }
   rc = attend_shape(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, cap);
   if (rc != LSA_OK) return rc;
   if (!(std::fabs(sm_scale) <= 3.4e38f)) return fail(LSA_ERR_INVALID_ARG, "kv_attend: sm_scale is not finite");

@@ -1,4 +1,4 @@
-// Attention over the 8-bit KV cache on the tensor cores of sm_100a: TMA row gathers ->
+// Attention over the 8-bit KV cache on the tensor cores of sm_100a: TMA boxes or copies of rows ->
 // shared memory -> tcgen05.mma -> tensor memory, one pass with a running reference exponent.
 //
 // The cached codes are the MMA's operands as they lie in memory: nothing is decoded to 16
@@ -28,12 +28,22 @@
 // multiplied by 2^(r_old - r_new) in tensor memory.  That is rare after the first tile, so the
 // cross-lane maxima are only computed then; otherwise a tile costs one vote.
 //
-// Roles (10, 14 or 22 warps by the columns): warps 0-3 bring the rows, one token a lane, chunk by
-// chunk, and write the tokens' scales; four warps for each 16 columns hold one token a lane; the last warp issues the MMAs, S a tile ahead of O, a chunk at a time as chunks
-// arrive.  A warp whose 32 rows follow one another in memory (a dense cache, pages of 16 and
-// more) brings them as TMA boxes; other rows (a fetched list) go by 16-byte asynchronous
-// copies in the MMA's swizzle, with zeros where a place has no token.  TMA row gathers were
-// slower: 65 clocks a four-row instruction, 8 bytes a clock and SM, a third of the HBM rate.
+// Roles (10, 14 or 22 warps by the columns).  Warps 0-3 bring the rows, one token a lane, chunk
+// by chunk, and write the tokens' scales.  Four warps for each 16 columns make the weights, one
+// token a lane.  The last two issue the MMAs of S and of O, a chunk at a time as chunks arrive and
+// weights are ready, S a tile ahead of O.  Rows that follow one another in memory (a dense
+// cache, pages of 16 and more) come as TMA boxes; other rows (a fetched list) by 16-byte
+// asynchronous copies in the MMA's swizzle, with zeros where a place has no token: with 64 KB
+// in flight an SM, random 128-byte pieces come at 19 bytes a clock by copies and at 13 by TMA row
+// gathers.
+//
+// What bounds it.  With few query columns, memory: 16384 tokens x 8 KV heads x 256 bytes, B = 32,
+// read at 5.1 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
+// rate (an MMA of N = 128 takes 64 clocks, of N = 64 48: its operands' bytes), and the chain of a
+// tile (rows 0.9 us, S 0.6 to 1.5, weights 1.4, O 0.8 to 1.4) over the two tiles that fit beside
+// the query image comes to 2.5 to 2.8 us, against 1.7 for its bytes.  The join of a cluster is bound by
+// distributed shared memory (14 to 16 bytes a clock and SM however it is moved): 5 us for 64
+// columns of 512 values in four blocks, which is why short calls take fewer columns a block.
 //
 // A sequence's tokens are divided among the blocks of a cluster (and, when there are few
 // sequences, among several clusters).  At the end each block lays its O^T and sums in its
@@ -342,7 +352,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     u = q;
     return static_cast<int>(r);
   };
-  pdl_wait();                                              // what follows reads the call's inputs
+  pdl_wait();      // what follows reads the call's inputs (by plain loads: the kernel before may have written them while this one started)
   const int rank = digit(t.cluster), cg = digit(t.col_groups), grp = digit(a.splits), head = digit(g.G);   // a.splits: clusters of a unit
   const int b = static_cast<int>(u);
   const int c_base = cg * C, n_c = min(C, ncol - c_base);
@@ -412,8 +422,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       page = -1;
       sc = 0.f;
       if (tok < 0) return;
-      page = g.table != nullptr ? __ldg(g.table + static_cast<size_t>(b) * g.n_pages + (tok >> g.page_log)) : tok >> g.page_log;
-      sc = __ldg(g.scale + kv_scale_at(g, b, tok, head));
+      page = g.table != nullptr ? g.table[static_cast<size_t>(b) * g.n_pages + (tok >> g.page_log)] : tok >> g.page_log;
+      sc = g.scale[kv_scale_at(g, b, tok, head)];
     };
     // The token's row (-1: nothing to read), scale (0: nobody sees it) and word.
     auto settle = [&](int tok, bool main, int page, float sc) {
@@ -562,7 +572,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     }
     // every copy has landed before the block goes on: on the way out of an abort too
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok) drain_boxes();
+    if (*abort_flag) drain_boxes();
   } else if (warp >= kMmaWarp) {
     // ---------------------------------------------------------------- MMA issuers
     // One warp for the scores and one for the values: an issue waits while the tensor core is
@@ -673,7 +683,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const int e = (lane + 32 * k) * 8;
-            v[k2][k] = c < n_c && e < a.d ? __ldg(reinterpret_cast<const uint4*>(qrow + e)) : make_uint4(0, 0, 0, 0);
+            v[k2][k] = c < n_c && e < a.d ? *reinterpret_cast<const uint4*>(qrow + e) : make_uint4(0, 0, 0, 0);
           }
         }
         float inv[kBatch];

@@ -22,7 +22,7 @@ struct KvGeom {
 // has no page for it or the page lies outside the pool.
 __device__ __forceinline__ long long kv_row(const KvGeom& g, int b, int t) {
   int p = t >> g.page_log;
-  if (g.table != nullptr) p = __ldg(g.table + static_cast<size_t>(b) * g.n_pages + p);
+  if (g.table != nullptr) p = g.table[static_cast<size_t>(b) * g.n_pages + p];
   if (p < 0 || (g.seq_pages > 0 && p >= g.seq_pages)) return -1;
   const long long phys = static_cast<long long>(b) * g.seq_pages + p;
   if (phys >= g.pages) return -1;
@@ -62,8 +62,8 @@ struct KvSpan {
 
 __device__ __forceinline__ KvSpan kv_span(const KvAttendArgs& a, int b) {
   KvSpan s;
-  s.len = min(max(__ldg(a.length + b), 0), a.g.N);
-  const int listed = a.idx != nullptr ? max(0, min(__ldg(a.count + b), a.cap)) : 0;
+  s.len = min(max(a.length[b], 0), a.g.N);
+  const int listed = a.idx != nullptr ? max(0, min(a.count[b], a.cap)) : 0;
   s.first = s.pad = s.lo = s.start = 0;
   s.n_main = s.len;
   if (a.window >= 0) {
@@ -94,7 +94,7 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
     const int t = s.start + (v - s.pad);
     return t < s.lo ? -1 : t;
   }
-  const int e = __ldg(a.idx + static_cast<size_t>(b) * a.cap + (v - s.n_main));
+  const int e = a.idx[static_cast<size_t>(b) * a.cap + (v - s.n_main)];
   if (e >= s.len) {
     raise_status(a.status, LSA_ERR_RANGE);
     return -1;

@@ -108,3 +108,21 @@ def test_binding_refuses_host_tensors_types_and_short_arrays(lib):
         lsa._dev(torch.zeros(4, dtype=torch.int64), "idx", (torch.int32,), 4, 0)
     with pytest.raises(ValueError, match="one CUDA device"):
         lsa.lsa_rope(2, 1, 8, 0, 1, x, 64, 8, i, torch.zeros(4, dtype=torch.float64), 1.0, 0, x, 64, 8, stream=0)
+
+
+def test_binding_refuses_views_it_cannot_walk():
+    """Strided sources are walked with the call's strides: the last dimension must be dense and the
+    span must lie in the storage (checked on the host's own tensors; nothing is launched)."""
+    x = torch.zeros(4, 6, 64)
+    d = x.get_device()
+    ok = lambda t, span: lsa._bad(t, "x", lsa._QTYPES, span, d)  # noqa: E731
+    assert "one CUDA device" in ok(x, 0)
+    class Fake(torch.Tensor):
+        def get_device(self):
+            return 0
+    f = x.as_subclass(Fake)
+    assert lsa._dev_strided(f, "x", lsa._QTYPES, x.numel(), 0) == x.data_ptr()
+    assert lsa._dev_strided(f[:, :, 32:], "x", lsa._QTYPES, x.numel() - 32, 0) == x.data_ptr() + 128
+    for t, span in ((f, x.numel() + 1), (f[1:], x.numel()), (f, -1), (f.transpose(1, 2), 8)):
+        with pytest.raises(ValueError):
+            lsa._dev_strided(t, "x", lsa._QTYPES, span, 0)
