@@ -9,6 +9,7 @@
 //
 // Both kernels move each byte once and are bound by memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_common.cuh"
 
@@ -16,6 +17,7 @@ namespace lsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFlight = 4;            // vectors a lane of the read has in flight
 constexpr uint32_t kNanBits = 0x7fc00000u;
 
 // Eight consecutive elements as they lie in memory.
@@ -263,43 +265,73 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 32 bytes in one store.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+    store32(p + 8 * h, w);
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  store32(p, w);
+}
 // A warp reads 2^tpw_log listed tokens.  Its lanes look the tokens up first (list entry, page and,
-// with one head, scale), then take the tokens' rows together, eight codes a lane (16 bytes of
-// bf16 out, so that a warp's stores are whole sectors), four in flight.
-template <typename T>
+// with one head, scale; the list's entry does not wait for the count), then take the tokens'
+// rows together, kFlight vectors a lane in flight.  kWide: 16 codes a lane (32 bytes of bf16 out in
+// one store), where the row width and the buffers allow it; else eight.  Bound by memory: 100 MB of
+// random 576-byte rows and their bf16 take 22.6 us (4.4 TB/s; 23.5 with eight codes a lane),
+// of 15.3 at the copy rate; more vectors in flight, or all 64 warps on an SM, change nothing.
+template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads)
 kv_read_kernel(const KvGeom g, const int32_t* __restrict__ idx, int cap, const int32_t* __restrict__ count,
                T* __restrict__ out, int32_t* status, uint32_t warps_per_seq, int tpw_log) {
-  const uint32_t vpr = g.W / 8, vpt = g.G * vpr;   // vectors of a row and of a token
+  constexpr int V = kWide ? 16 : 8;
+  using Code = std::conditional_t<kWide, uint4, uint2>;
+  const uint32_t vpr = g.W / V, vpt = g.G * vpr;   // vectors of a row and of a token
   const uint32_t warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t b = warp / warps_per_seq;
   if (b >= static_cast<uint32_t>(g.B)) return;
-  const int n = count != nullptr ? min(max(__ldg(count + b), 0), cap) : cap;
   const int j0 = static_cast<int>((warp - b * warps_per_seq) << tpw_log);
+  int tok = -1, row = -1;
+  if (lane < (1u << tpw_log) && j0 + static_cast<int>(lane) < cap)
+    tok = idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j0 + lane) : j0 + static_cast<int>(lane);
+  const int n = count != nullptr ? min(max(__ldg(count + b), 0), cap) : cap;
   const int mine = min(1 << tpw_log, n - j0);      // tokens of this warp; what lies behind the count is left alone
   if (mine <= 0) return;
-  int tok = -1, row = -1;
   float scale = 0.f;
   if (static_cast<int>(lane) < mine) {
-    tok = idx != nullptr ? __ldg(idx + static_cast<size_t>(b) * cap + j0 + lane) : j0 + static_cast<int>(lane);
     if (tok >= 0) {
       if (tok < g.N) {
-        row = static_cast<int>(kv_row(g, b, tok));
         scale = __ldg(g.scale + kv_scale_at(g, b, tok, 0));
+        row = static_cast<int>(kv_row(g, b, tok));
       }
       if (row < 0) raise_status(status, LSA_ERR_RANGE);
     }
   }
-  T* const to = out + (static_cast<size_t>(b) * cap + j0) * vpt * 8 + lane * 8;
+  T* const to = out + (static_cast<size_t>(b) * cap + j0) * vpt * V + lane * V;
   const uint32_t total = mine * vpt;
   uint32_t tk = 0, c = lane;                       // token of this lane's vector, and the vector in it
   while (c >= vpt) { c -= vpt; ++tk; }
-  for (uint32_t v0 = 0; v0 < total; v0 += 128) {
-    uint2 code[4];
-    float s[4];
-    bool there[4];
+  for (uint32_t v0 = 0; v0 < total; v0 += 32 * kFlight) {
+    Code code[kFlight];
+    float s[kFlight];
+    bool there[kFlight];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kFlight; ++k) {
       const int from = min(tk, 31u);
       const int r = __shfl_sync(0xffffffffu, row, from);
       s[k] = __shfl_sync(0xffffffffu, scale, from);
@@ -307,20 +339,20 @@ kv_read_kernel(const KvGeom g, const int32_t* __restrict__ idx, int cap, const i
       there[k] = v0 + k * 32 + lane < total && r >= 0;
       if (there[k]) {
         if (g.G > 1) s[k] = __ldg(g.scale + kv_scale_at(g, b, t, c / vpr));
-        code[k] = *reinterpret_cast<const uint2*>(g.rows + (static_cast<size_t>(r) * vpt + c) * 8);
+        code[k] = __ldg(reinterpret_cast<const Code*>(g.rows + (static_cast<size_t>(r) * vpt + c) * V));
       }
       c += 32;
       while (c >= vpt) { c -= vpt; ++tk; }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kFlight; ++k) {
       if (!there[k]) continue;
-      float f[8];
-      decode2(code[k].x & 0xffffu, s[k], f[0], f[1]);
-      decode2(code[k].x >> 16, s[k], f[2], f[3]);
-      decode2(code[k].y & 0xffffu, s[k], f[4], f[5]);
-      decode2(code[k].y >> 16, s[k], f[6], f[7]);
-      store8(to + static_cast<size_t>(v0 + k * 32) * 8, f);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&code[k]);
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) decode2((w[i / 2] >> (i % 2 * 16)) & 0xffffu, s[k], f[2 * i], f[2 * i + 1]);
+      if constexpr (kWide) store16(to + static_cast<size_t>(v0 + k * 32) * V, f);
+      else store8(to + static_cast<size_t>(v0 + k * 32) * V, f);
     }
   }
 }
@@ -361,16 +393,22 @@ int launch_kv_write(const KvGeom& g, int T, int xdt, const void* x, size_t x_str
 
 int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* count, int odt, void* out,
                    int32_t* status, cudaStream_t s) {
-  // As many tokens a warp (up to 8) as leave 64 warps for each SM (65536 rows: 23.4 us with 4 tokens a
-  // warp, 25.2 with 2 and with 8, 29.8 with one).
+  // As many tokens a warp (up to 4) as leave 64 warps for each SM (those rows: 22.6 us with 4 tokens a
+  // warp and with 8, 25.4 with 2).
   int tpw = 0;
-  while (tpw < 3 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 64 * 148) ++tpw;
+  while (tpw < 2 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 64 * 148) ++tpw;
   const long long per_seq = (cap + (1ll << tpw) - 1) >> tpw, warps = per_seq * g.B;
   if (warps > 0x7fffffffll || static_cast<long long>(g.G) * (g.W / 8) > (1 << 24))
     return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap = %lld, G * W = %lld (at most 2^31, 2^27)", static_cast<long long>(g.B) * cap, static_cast<long long>(g.G) * g.W);
   const unsigned grid = static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)), ps = static_cast<unsigned>(per_seq);
-  if (odt == LSA_F32) kv_read_kernel<float><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);
-  else kv_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, ps, tpw);
+  const bool wide = g.W % 16 == 0 && aligned(g.rows, 16) && aligned(out, 32);
+  if (odt == LSA_F32) {
+    if (wide) kv_read_kernel<float, true><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);
+    else kv_read_kernel<float, false><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);
+  } else {
+    if (wide) kv_read_kernel<__nv_bfloat16, true><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, ps, tpw);
+    else kv_read_kernel<__nv_bfloat16, false><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<__nv_bfloat16*>(out), status, ps, tpw);
+  }
   return check_launch("kv_read");
 }
 
