@@ -48,7 +48,7 @@ int make_geom(const char* who, int B, int N, int G, int W, int block, int page, 
 
 struct AttendWs {
   int cols;          // query columns of a block on the tensor cores, 0: CUDA cores
-  int cluster, splits;
+  int cluster, team, splits;
   size_t o, m, l, total;
 };
 
@@ -61,7 +61,7 @@ AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, 
   w.cols = N <= (1 << 30) ? kv_attend_columns_tc(b1, G, n1, most, d, dv, voff, qdt) : 0;   // token words have 30 bits
   w.cluster = 1;
   if (w.cols > 0) kv_attend_parts_tc(b1, G, n1, w.cols, d, dv, voff, most, w.cluster, w.splits);
-  else w.splits = kv_attend_splits_simt(b1, G, n1, most);
+  else kv_attend_parts_simt(b1, G, n1, most, w.team, w.splits);
   const size_t cols = static_cast<size_t>(B) * G * w.splits * ncol;
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off = align_up(off + bytes, 256); return at; };
@@ -185,7 +185,7 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
   a.part_m = reinterpret_cast<float*>(base + ws.m);
   a.part_l = reinterpret_cast<float*>(base + ws.l);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = ws.cols > 0 ? launch_kv_attend_tc(a, ws.cols, ws.cluster, st) : launch_kv_attend_simt(a, st);
+  rc = ws.cols > 0 ? launch_kv_attend_tc(a, ws.cols, ws.cluster, st) : launch_kv_attend_simt(a, ws.team, st);
   if (rc != LSA_OK || a.splits == 1) return rc;
   return launch_kv_attend_combine(a, st);
 }

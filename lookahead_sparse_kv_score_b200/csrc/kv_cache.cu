@@ -292,7 +292,7 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) 
 // A warp reads 2^tpw_log listed tokens.  Its lanes look the tokens up first (list entry, page and,
 // with one head, scale; the list's entry does not wait for the count), then take the tokens'
 // rows together, kFlight vectors a lane in flight.  kWide: 16 codes a lane (32 bytes of bf16 out in
-// one store), where the row width and the buffers allow it; else eight.  Bound by memory: 100 MB of
+// one store) where the output's alignment allows it, else eight.  Bound by memory: 100 MB of
 // random 576-byte rows and their bf16 take 22.6 us (4.4 TB/s; 23.5 with eight codes a lane),
 // of 15.3 at the copy rate; more vectors in flight, or all 64 warps on an SM, change nothing.
 template <typename T, bool kWide>
@@ -401,7 +401,7 @@ int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* 
   if (warps > 0x7fffffffll || static_cast<long long>(g.G) * (g.W / 8) > (1 << 24))
     return fail(LSA_ERR_UNSUPPORTED, "kv_read: B * cap = %lld, G * W = %lld (at most 2^31, 2^27)", static_cast<long long>(g.B) * cap, static_cast<long long>(g.G) * g.W);
   const unsigned grid = static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32)), ps = static_cast<unsigned>(per_seq);
-  const bool wide = g.W % 16 == 0 && aligned(g.rows, 16) && aligned(out, 32);
+  const bool wide = aligned(out, 32);              // rows are multiples of 16 codes
   if (odt == LSA_F32) {
     if (wide) kv_read_kernel<float, true><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);
     else kv_read_kernel<float, false><<<grid, kThreads, 0, s>>>(g, idx, cap, count, static_cast<float*>(out), status, ps, tpw);

@@ -18,16 +18,21 @@ struct KvGeom {
   float* scale;
 };
 
-// Row of token t (0 <= t < N) of sequence b, in units of G * W bytes, or -1 where the table
-// has no page for it or the page lies outside the pool.
-__device__ __forceinline__ long long kv_row(const KvGeom& g, int b, int t) {
-  int p = t >> g.page_log;
-  if (g.table != nullptr) p = g.table[static_cast<size_t>(b) * g.n_pages + p];
+// Page of token t (0 <= t < N) of sequence b as the table has it.
+__device__ __forceinline__ int kv_page(const KvGeom& g, int b, int t) {
+  const int p = t >> g.page_log;
+  return g.table != nullptr ? g.table[static_cast<size_t>(b) * g.n_pages + p] : p;
+}
+
+// Row of a token on page p, in units of G * W bytes, or -1 where the table has no page for it or
+// the page lies outside the pool.
+__device__ __forceinline__ long long kv_row_of(const KvGeom& g, int b, int t, int p) {
   if (p < 0 || (g.seq_pages > 0 && p >= g.seq_pages)) return -1;
   const long long phys = static_cast<long long>(b) * g.seq_pages + p;
   if (phys >= g.pages) return -1;
   return (phys << g.page_log) + (t & ((1 << g.page_log) - 1));
 }
+__device__ __forceinline__ long long kv_row(const KvGeom& g, int b, int t) { return kv_row_of(g, b, t, kv_page(g, b, t)); }
 
 __device__ __forceinline__ size_t kv_scale_at(const KvGeom& g, int b, int t, int head) {
   return (static_cast<size_t>(b) * g.n_blocks + (t >> g.block_log)) * g.G + head;
@@ -107,8 +112,9 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
 int kv_attend_columns_tc(int B, int G, int ncol, long long max_tokens, int d, int dv, int voff, int qdt);
 void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, long long max_tokens, int& cluster, int& groups);
 int launch_kv_attend_tc(const KvAttendArgs& a, int C, int cluster, cudaStream_t s);
-int kv_attend_splits_simt(int B, int G, int ncol, long long max_tokens);
-int launch_kv_attend_simt(const KvAttendArgs& a, cudaStream_t s);
+// The CUDA-core path: warps of a column, and parts of a unit's tokens (KvAttendArgs::splits).
+void kv_attend_parts_simt(int B, int G, int ncol, long long max_tokens, int& team, int& splits);
+int launch_kv_attend_simt(const KvAttendArgs& a, int team, cudaStream_t s);
 int launch_kv_attend_combine(const KvAttendArgs& a, cudaStream_t s);
 
 // ------------------------------------------------------------------ cache and rotation

@@ -247,3 +247,42 @@ def test_guards_kv(dtype, d, dv, voff, W, hg):
     torch.cuda.synchronize()
     for t in (rows, scale, out, lse, st, ws, back, ro):
         assert t.intact()
+
+
+@pytest.mark.parametrize("B,G,hg,d,dv,voff,W,N,cap", [
+    (1, 1, 8, 576, 512, 0, 576, 500, 0),       # few columns: every warp of a block on one
+    (1, 1, 1, 576, 512, 512, 1024, 200, 0),    # rows wider than what is read ahead
+    (2, 2, 3, 36, 60, 100, 176, 333, 0),       # a short score, shared out among two warps
+    (2, 1, 11, 33, 31, 34, 80, 150, 20),       # columns that take no vectors, with a list
+    (75, 2, 8, 64, 64, 64, 128, 70, 40),       # blocks for every SM: a warp a column
+    (30, 1, 16, 96, 80, 96, 176, 130, 9)])
+def test_attend_f32_teams(B, G, hg, d, dv, voff, W, N, cap):
+    """fp32 queries over every division of a block's warps among columns."""
+    c = K.Cache(d, B, N, G, W, 4, 8, "slots")
+    g = np.random.default_rng(B)
+    q = torch.from_numpy(g.standard_normal((B, 2, G * hg, d))).float().cuda()
+    length = [max(2, N - 13 * b) for b in range(B)]
+    idx = count = None
+    if cap:
+        idx = np.stack([g.integers(-1, n, size=cap) for n in length]).astype(np.int32)
+        count = g.integers(0, cap + 1, size=B)
+    K.check_attend(c, q, d ** -0.5, length, 3 if cap else 0, 50 if cap else -1, idx, count, d, dv, voff)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_read_to_any_aligned_output(dtype):
+    """Outputs on 16 bytes that are not on 32 get the same rows as others."""
+    B, N, G, W, cap = 3, 90, 2, 48, 37
+    c = K.Cache(8, B, N, G, W, 4, 8, "paged")
+    idx = K.i32(np.random.default_rng(1).integers(-1, N, size=(B, cap)))
+    count = K.i32([cap, 11, 0])
+    n, step = B * cap * G * W, 128 // torch.finfo(dtype).bits
+    outs = []
+    for off in (0, step):
+        buf = torch.full((n + 2 * step,), 5.0, dtype=dtype, device="cuda")
+        lsa.lsa_kv_read(B, N, G, W, idx, cap, count, *c.args(), lsa.dtype_code(dtype), buf[off: off + n])
+        torch.cuda.synchronize()
+        assert (buf[:off] == 5).all() and (buf[off + n:] == 5).all()
+        outs.append(buf[off: off + n])
+    assert (outs[0].data_ptr() % 32, outs[1].data_ptr() % 32) == (0, 16)
+    assert torch.equal(outs[0], outs[1]) and (outs[0] != 5).any()
