@@ -38,7 +38,7 @@
 // gathers.
 //
 // What bounds it.  With few query columns, memory: 16384 tokens x 8 KV heads x 256 bytes, B = 32,
-// read at 5.1 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
+// read at 5.3 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
 // rate (an MMA of N = 128 takes 64 clocks, of N = 64 48: its operands' bytes), and the chain of a
 // tile (rows 0.9 us, S 0.6 to 1.5, weights 1.4, O 0.8 to 1.4) over the two tiles that fit beside
 // the query image comes to 2.5 to 2.8 us, against 1.7 for its bytes.  The join of a cluster is bound by
@@ -266,9 +266,12 @@ __device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t 
 __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint64_t normal_policy() {
+// L2 policy of the rows' boxes: rows that one block reads leave first (16384 tokens x 8 KV heads, B = 32:
+// 155 us, 158 without), rows that several blocks of a unit read do not.
+__device__ __forceinline__ uint64_t rows_policy(bool once) {
   uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 // After an abort the barriers of boxes in flight may never complete: a millisecond, far above
@@ -403,7 +406,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     const int p_first = sp.len - a.Tq + (c_base / hg), p_last = sp.len - a.Tq + (c_base + n_c - 1) / hg;
     const int n_kf = pl.n_k - pl.tail, gap = max(pl.v0 - n_kf, 0);   // chunks between keys and values are not read
     const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
-    const uint64_t policy = normal_policy();
+    const uint64_t policy = rows_policy(t.col_groups == 1);
     const int v_slot0 = plan_v_slot(pl, pl.v0);
     const bool divide = t.run > 0 && pl.n_full >= 3;
     const int piece = lane & 7, r_in = lane >> 3;          // a lane's 16 bytes of a chunk and its row of four
