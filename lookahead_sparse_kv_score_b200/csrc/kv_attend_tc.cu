@@ -38,7 +38,7 @@
 // gathers.
 //
 // What bounds it.  With few query columns, memory: 16384 tokens x 8 KV heads x 256 bytes, B = 32,
-// read at 5.3 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
+// read at 5.5 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
 // rate (an MMA of N = 128 takes 64 clocks, of N = 64 48: its operands' bytes), and the chain of a
 // tile (rows 0.9 us, S 0.6 to 1.5, weights 1.4, O 0.8 to 1.4) over the two tiles that fit beside
 // the query image comes to 2.5 to 2.8 us, against 1.7 for its bytes.  The join of a cluster is bound by
@@ -176,11 +176,17 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
                "%14, %15}, [%16];" : LSA_R8(r, 0), LSA_R8(r, 8) : "r"(t));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : LSA_R8(r, 0) : "r"(t));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t& r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(t));
 }
 __device__ __forceinline__ void tmem_st(uint32_t t, uint32_t r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(r), "r"(t) : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::LSA_I8(r, 0), "r"(t) : "memory");
 }
 __device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
@@ -267,7 +273,7 @@ __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // L2 policy of the rows' boxes: rows that one block reads leave first (16384 tokens x 8 KV heads, B = 32:
-// 155 us, 158 without), rows that several blocks of a unit read do not.
+// 2% less time), rows that several blocks of a unit read do not.
 __device__ __forceinline__ uint64_t rows_policy(bool once) {
   uint64_t p;
   if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -308,6 +314,11 @@ __device__ __forceinline__ void split2(float2 p, uint32_t& hi, uint32_t& lo) {
   hi = h;
   lo = __nv_cvt_float2_to_fp8x2(make_float2(p.x - f.x, p.y - f.y), __NV_SATFINITE, __NV_E5M2);
 }
+
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[2]) { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
 
 // Blocks of a unit: rank (fastest), column group, cluster of the unit's parts, KV head, sequence.
 template <int C>
@@ -744,195 +755,203 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       if (lane == 0) mbar_arrive(qfull);
       asm volatile("barrier.cta.sync 5, %0;" ::"n"(32 * Sh::kWeights) : "memory");   // the columns' factors, to all
     }
-    // Scratch of 512 words for the group, in its own columns' block of the weights buffer, while no
-    // MMA reads it.
-    auto scratch = [&](int i) { return reinterpret_cast<float*>(pbuf + wg * 2048) + i; };
-    float2 l[NC / 2];
+    // NA: 16 (NC), or 8 where the block has no more columns (what lies behind is not read): 16384 tokens x 8 KV
+    // heads of 8 columns, B = 32, take 147 us, 154 with 16.  One group of several on its own code is
+    // slower (20 columns, 4096 tokens x 7 heads, B = 8: 33.6 us, 31.1 with 16 in both).
+    auto weigh = [&](auto active) {
+      constexpr int NA = decltype(active)::value;
+      // Scratch of 512 words for the group, in its own columns' block of the weights buffer, while no
+      // MMA reads it.
+      auto scratch = [&](int i) { return reinterpret_cast<float*>(pbuf + wg * 2048) + i; };
+      float2 l[NA / 2];
 #pragma unroll
-    for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
-    const float target = fminf(fmaxf(lg2(static_cast<float>(max(n, 1))) - 1.f, 0.f), 6.f);   // log2(128 n) - 8
-    bool ok = true;
-    int s = 0;
-    uint32_t ph = 0;
+      for (int c = 0; c < NA / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      const float target = fminf(fmaxf(lg2(static_cast<float>(max(n, 1))) - 1.f, 0.f), 6.f);   // log2(128 n) - 8
+      bool ok = true;
+      int s = 0;
+      uint32_t ph = 0;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      if (ok) ok = mbar_wait(&ifull[s], ph, abort_flag);
-      const float2 in = info[s * kTile + row];
-      const float scale = in.x;
-      const int word = __float_as_int(in.y);
-      // an unseen token has scale 0: its exponent is 0 + log2(0) = -infinity
-      const float ls = scale == 0.f ? -INFINITY : lg2(scale);
-      uint32_t seen = 0xffffffffu;                         // columns of this group that see the token
-      if (a.Tq > 1 && !__all_sync(0xffffffffu, word < 0 || scale == 0.f)) {
-        if (word >= 0) {
-          seen = 0;
+      for (int j = 0; j < n; ++j) {
+        if (ok) ok = mbar_wait(&ifull[s], ph, abort_flag);
+        const float2 in = info[s * kTile + row];
+        const float scale = in.x;
+        const int word = __float_as_int(in.y);
+        // an unseen token has scale 0: its exponent is 0 + log2(0) = -infinity
+        const float ls = scale == 0.f ? -INFINITY : lg2(scale);
+        uint32_t seen = 0xffffffffu;                         // columns of this group that see the token
+        if (a.Tq > 1 && !__all_sync(0xffffffffu, word < 0 || scale == 0.f)) {
+          if (word >= 0) {
+            seen = 0;
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            const bool in_main = kv_sees(a, word & (kListFlag - 1), sp.len - a.Tq + qi[c0 + c]);
-            seen |= (in_main != ((word & kListFlag) != 0) ? 1u : 0u) << c;
-          }
-        }
-      }
-      if (ok) ok = mbar_wait(&sfull[j & 1], (j >> 1) & 1, abort_flag);
-      tc_fence_after();
-      // Exponents above the reference (pass 0 and 2) or as they are (pass 1: the reference is set
-      // anew, for the first tile and when a weight passes its limit).
-      float y[NC];
-      bool stop = false;
-#pragma unroll 1
-      for (int pass = j == 0 ? 1 : 0; pass < 3; ++pass) {
-        const float2 with_ref = pass == 1 ? make_float2(0.f, 0.f) : make_float2(1.f, 1.f);
-        uint32_t hi[NC], lo[NC];
-        const uint32_t st = tmem + lanes + (j & 1) * (2 * C) + c0;
-        tmem_ld(st, hi);
-        tmem_ld(st + C, lo);
-        tmem_wait_ld();
-        const float2 ls2 = make_float2(ls, ls), sc2 = make_float2(scale, scale);
-#pragma unroll
-        for (int c = 0; c < NC; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(qf + c0 + c), r = *reinterpret_cast<const float4*>(nref + c0 + c);
-          const float2 x0 = mul2(add2(pair(hi[c], hi[c + 1]), pair(lo[c], lo[c + 1])), sc2);
-          const float2 x1 = mul2(add2(pair(hi[c + 2], hi[c + 3]), pair(lo[c + 2], lo[c + 3])), sc2);
-          const float2 y0 = fma2(x0, make_float2(f.x, f.y), fma2(make_float2(r.x, r.y), with_ref, ls2));
-          const float2 y1 = fma2(x1, make_float2(f.z, f.w), fma2(make_float2(r.z, r.w), with_ref, ls2));
-          y[c] = y0.x;
-          y[c + 1] = y0.y;
-          y[c + 2] = y1.x;
-          y[c + 3] = y1.y;
-        }
-        if (seen != 0xffffffffu) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (!((seen >> c) & 1)) y[c] = -INFINITY;
-        }
-        if (pass == 2) break;
-        if (pass == 0) {
-          float top = y[0];
-#pragma unroll
-          for (int c = 1; c < NC; ++c) top = fmaxf(top, y[c]);
-          if (!group_any(bar_id, !ok || top > kLimit)) break;
-          continue;
-        }
-        stop = group_any(bar_id, !ok);                     // the same for the whole group
-        if (stop) break;
-        // The weights buffer is scratch once the MMAs that read it are done.
-        if (j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
-        tc_fence_after();
-        float mine = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float m = warp_max(y[c]);
-          if (lane == c) mine = m;
-        }
-        if (lane < NC) *scratch(quad * 32 + lane) = mine;
-        group_sync(bar_id);
-        float f_mine = 1.f, now = 0.f;
-        if (lane < NC) {
-          const float old = nref[c0 + lane];
-          const float m = fmaxf(fmaxf(*scratch(lane), *scratch(32 + lane)), fmaxf(*scratch(64 + lane), *scratch(96 + lane)));
-          now = m + old > kLimit ? target - m : old;
-          f_mine = now == old ? 1.f : ex2(now - old);      // 0 from unset
-        }
-        group_sync(bar_id);                                // every warp has read the old reference
-        if (quad == 0 && lane < NC) nref[c0 + lane] = now;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) (c & 1 ? l[c / 2].y : l[c / 2].x) *= __shfl_sync(0xffffffffu, f_mine, c);
-        const uint32_t moved = __ballot_sync(0xffffffffu, f_mine != 1.f);   // columns whose reference moved
-        if (j > 0) {
-#pragma unroll 1
-          for (int m = 0; m < pl.n_v; ++m) {
-            const uint32_t at = tmem + lanes + kO + m * C + c0;
-            if (__popc(moved) > 4) {
-              tmem_ld(at, hi);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < NC; ++c) hi[c] = __float_as_uint(__uint_as_float(hi[c]) * __shfl_sync(0xffffffffu, f_mine, c));
-              tmem_st(at, hi);
-            } else {
-              for (uint32_t left = moved; left != 0; left &= left - 1) {
-                const int c = __ffs(left) - 1;
-                uint32_t o;
-                tmem_ld(at + c, o);
-                tmem_wait_ld();
-                tmem_st(at + c, __float_as_uint(__uint_as_float(o) * __shfl_sync(0xffffffffu, f_mine, c)));
-              }
+            for (int c = 0; c < NA; ++c) {
+              const bool in_main = kv_sees(a, word & (kListFlag - 1), sp.len - a.Tq + qi[c0 + c]);
+              seen |= (in_main != ((word & kListFlag) != 0) ? 1u : 0u) << c;
             }
           }
-          tmem_wait_st();
         }
-        group_sync(bar_id);                                // the new reference, to all
-      }
-      if (stop) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sempty[j & 1]);
-      // Of a NaN scale only the columns that see the token become NaN.
-      const float inv = scale > 0.f ? 1.0f / scale : 1.0f;
-      uint32_t hw[NC / 4], lw[NC / 4];
-#pragma unroll
-      for (int c = 0; c < NC; c += 4) {
-        const float2 p0 = make_float2(ex2(y[c]), ex2(y[c + 1])), p1 = make_float2(ex2(y[c + 2]), ex2(y[c + 3]));
-        const float2 inv2 = make_float2(inv, inv);
-        l[c / 2] = fma2(p0, inv2, l[c / 2]);
-        l[c / 2 + 1] = fma2(p1, inv2, l[c / 2 + 1]);
-        uint32_t h0, h1, l0, l1;
-        split2(p0, h0, l0);
-        split2(p1, h1, l1);
-        hw[c / 4] = h0 | (h1 << 16);
-        lw[c / 4] = l0 | (l1 << 16);
-      }
-      if (ok && j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
-      uint8_t* pr = pbuf + wg * 2048 + row * 16;
-      *reinterpret_cast<uint4*>(pr) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      *reinterpret_cast<uint4*>(pr + (C / 16) * 2048) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pfull);
-      if (++s == pl.stages) { s = 0; ph ^= 1; }
-    }
-    // The last tile's values are in.  Sums over the block's tokens, and O^T into the ring as
-    // [C][128 n_v] fp32 (every tile has been read).
-    if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
-    tc_fence_after();
-    // Each step halves the columns a lane holds; lane l ends with column l / 2.
-    float v[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
-    int o = 16;
-#pragma unroll
-    for (int w = NC / 2; w >= 1; w /= 2) {
-#pragma unroll
-      for (int c = 0; c < w; ++c) {
-        const bool up = (lane & o) != 0;
-        const float keep = up ? v[c + w] : v[c], give = up ? v[c] : v[c + w];
-        v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-      }
-      o >>= 1;
-    }
-    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-    *scratch(quad * 32 + (lane >> 1)) = v[0];
-    group_sync(bar_id);
-    if (quad == 0 && lane < NC)
-      qf[c0 + lane] = (*scratch(lane) + *scratch(32 + lane)) + (*scratch(64 + lane) + *scratch(96 + lane));
-    float* os = reinterpret_cast<float*>(ring) + row;
-    const int pitch = pl.n_v * 128;
+        if (ok) ok = mbar_wait(&sfull[j & 1], (j >> 1) & 1, abort_flag);
+        tc_fence_after();
+        // Exponents above the reference (pass 0 and 2) or as they are (pass 1: the reference is set
+        // anew, for the first tile and when a weight passes its limit).
+        float y[NA];
+        bool stop = false;
 #pragma unroll 1
-    for (int m = 0; m < pl.n_v; ++m) {
-      uint32_t o[NC];
+        for (int pass = j == 0 ? 1 : 0; pass < 3; ++pass) {
+          const float2 with_ref = pass == 1 ? make_float2(0.f, 0.f) : make_float2(1.f, 1.f);
+          uint32_t hi[NA], lo[NA];
+          const uint32_t st = tmem + lanes + (j & 1) * (2 * C) + c0;
+          tmem_ld(st, hi);
+          tmem_ld(st + C, lo);
+          tmem_wait_ld();
+          const float2 ls2 = make_float2(ls, ls), sc2 = make_float2(scale, scale);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) o[c] = 0u;
-      if (n > 0) {
-        tmem_ld(tmem + lanes + kO + m * C + c0, o);
-        tmem_wait_ld();
-      }
-      float* to = os + m * 128 + c0 * pitch;
+          for (int c = 0; c < NA; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(qf + c0 + c), r = *reinterpret_cast<const float4*>(nref + c0 + c);
+            const float2 x0 = mul2(add2(pair(hi[c], hi[c + 1]), pair(lo[c], lo[c + 1])), sc2);
+            const float2 x1 = mul2(add2(pair(hi[c + 2], hi[c + 3]), pair(lo[c + 2], lo[c + 3])), sc2);
+            const float2 y0 = fma2(x0, make_float2(f.x, f.y), fma2(make_float2(r.x, r.y), with_ref, ls2));
+            const float2 y1 = fma2(x1, make_float2(f.z, f.w), fma2(make_float2(r.z, r.w), with_ref, ls2));
+            y[c] = y0.x;
+            y[c + 1] = y0.y;
+            y[c + 2] = y1.x;
+            y[c + 3] = y1.y;
+          }
+          if (seen != 0xffffffffu) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        *to = __uint_as_float(o[c]);
-        to += pitch;
+            for (int c = 0; c < NA; ++c)
+              if (!((seen >> c) & 1)) y[c] = -INFINITY;
+          }
+          if (pass == 2) break;
+          if (pass == 0) {
+            float top = y[0];
+#pragma unroll
+            for (int c = 1; c < NA; ++c) top = fmaxf(top, y[c]);
+            if (!group_any(bar_id, !ok || top > kLimit)) break;
+            continue;
+          }
+          stop = group_any(bar_id, !ok);                     // the same for the whole group
+          if (stop) break;
+          // The weights buffer is scratch once the MMAs that read it are done.
+          if (j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
+          tc_fence_after();
+          float mine = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NA; ++c) {
+            const float m = warp_max(y[c]);
+            if (lane == c) mine = m;
+          }
+          if (lane < NA) *scratch(quad * 32 + lane) = mine;
+          group_sync(bar_id);
+          float f_mine = 1.f, now = 0.f;
+          if (lane < NA) {
+            const float old = nref[c0 + lane];
+            const float m = fmaxf(fmaxf(*scratch(lane), *scratch(32 + lane)), fmaxf(*scratch(64 + lane), *scratch(96 + lane)));
+            now = m + old > kLimit ? target - m : old;
+            f_mine = now == old ? 1.f : ex2(now - old);      // 0 from unset
+          }
+          group_sync(bar_id);                                // every warp has read the old reference
+          if (quad == 0 && lane < NA) nref[c0 + lane] = now;
+#pragma unroll
+          for (int c = 0; c < NA; ++c) (c & 1 ? l[c / 2].y : l[c / 2].x) *= __shfl_sync(0xffffffffu, f_mine, c);
+          const uint32_t moved = __ballot_sync(0xffffffffu, f_mine != 1.f);   // columns whose reference moved
+          if (j > 0) {
+#pragma unroll 1
+            for (int m = 0; m < pl.n_v; ++m) {
+              const uint32_t at = tmem + lanes + kO + m * C + c0;
+              if (__popc(moved) > 4) {
+                tmem_ld(at, hi);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < NA; ++c) hi[c] = __float_as_uint(__uint_as_float(hi[c]) * __shfl_sync(0xffffffffu, f_mine, c));
+                tmem_st(at, hi);
+              } else {
+                for (uint32_t left = moved; left != 0; left &= left - 1) {
+                  const int c = __ffs(left) - 1;
+                  uint32_t o;
+                  tmem_ld(at + c, o);
+                  tmem_wait_ld();
+                  tmem_st(at + c, __float_as_uint(__uint_as_float(o) * __shfl_sync(0xffffffffu, f_mine, c)));
+                }
+              }
+            }
+            tmem_wait_st();
+          }
+          group_sync(bar_id);                                // the new reference, to all
+        }
+        if (stop) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[j & 1]);
+        // Of a NaN scale only the columns that see the token become NaN.
+        const float inv = scale > 0.f ? 1.0f / scale : 1.0f;
+        uint32_t hw[NA / 4], lw[NA / 4];
+#pragma unroll
+        for (int c = 0; c < NA; c += 4) {
+          const float2 p0 = make_float2(ex2(y[c]), ex2(y[c + 1])), p1 = make_float2(ex2(y[c + 2]), ex2(y[c + 3]));
+          const float2 inv2 = make_float2(inv, inv);
+          l[c / 2] = fma2(p0, inv2, l[c / 2]);
+          l[c / 2 + 1] = fma2(p1, inv2, l[c / 2 + 1]);
+          uint32_t h0, h1, l0, l1;
+          split2(p0, h0, l0);
+          split2(p1, h1, l1);
+          hw[c / 4] = h0 | (h1 << 16);
+          lw[c / 4] = l0 | (l1 << 16);
+        }
+        if (ok && j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
+        uint8_t* pr = pbuf + wg * 2048 + row * 16;
+        store_words(pr, hw);
+        store_words(pr + (C / 16) * 2048, lw);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+        if (++s == pl.stages) { s = 0; ph ^= 1; }
       }
-    }
+      // The last tile's values are in.  Sums over the block's tokens, and O^T into the ring as
+      // [C][128 n_v] fp32 (every tile has been read).
+      if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
+      tc_fence_after();
+      // Each step halves the columns a lane holds; lane l ends with column l / (32 / NA).
+      float v[NA];
+#pragma unroll
+      for (int c = 0; c < NA; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
+      int o = 16;
+#pragma unroll
+      for (int w = NA / 2; w >= 1; w /= 2) {
+#pragma unroll
+        for (int c = 0; c < w; ++c) {
+          const bool up = (lane & o) != 0;
+          const float keep = up ? v[c + w] : v[c], give = up ? v[c] : v[c + w];
+          v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+        o >>= 1;
+      }
+      for (; o >= 1; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      *scratch(quad * 32 + lane / (32 / NA)) = v[0];
+      group_sync(bar_id);
+      if (quad == 0 && lane < NA)
+        qf[c0 + lane] = (*scratch(lane) + *scratch(32 + lane)) + (*scratch(64 + lane) + *scratch(96 + lane));
+      float* os = reinterpret_cast<float*>(ring) + row;
+      const int pitch = pl.n_v * 128;
+#pragma unroll 1
+      for (int m = 0; m < pl.n_v; ++m) {
+        uint32_t o[NA];
+#pragma unroll
+        for (int c = 0; c < NA; ++c) o[c] = 0u;
+        if (n > 0) {
+          tmem_ld(tmem + lanes + kO + m * C + c0, o);
+          tmem_wait_ld();
+        }
+        float* to = os + m * 128 + c0 * pitch;
+#pragma unroll
+        for (int c = 0; c < NA; ++c) {
+          *to = __uint_as_float(o[c]);
+          to += pitch;
+        }
+      }
+    };
+    if (C == NC && n_c <= NC / 2) weigh(std::integral_constant<int, NC / 2>{});
+    else weigh(std::integral_constant<int, NC>{});
   }
   pdl_trigger();
   tc_fence_before();
