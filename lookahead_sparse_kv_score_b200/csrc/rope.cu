@@ -11,7 +11,8 @@
 // Each element is read and written once, so memory bounds the kernel.  A block takes several
 // tokens at a time: first its threads compute the tokens' sines and cosines into shared memory
 // (shared by all heads), then each thread moves 16-byte vectors, two in flight for each pair
-// of halves.  Rows whose base, strides or width do not allow 16 bytes go pair by pair.
+// of halves.  Rows whose base, strides or width do not allow 16 bytes go pair by pair.  16384
+// tokens of 32 heads of 128 bf16 (268 MB) take 46.4 us, 5.8 TB/s; 32-byte vectors make it 47.6.
 #include <algorithm>
 
 #include "kv_common.cuh"
