@@ -87,6 +87,7 @@ constexpr int kTailBytes = kTile * 64;        // the last 64 key columns, 64-byt
 constexpr int kMaxStages = 4;
 constexpr int kMaxSlots = 12;                 // stages times 128-column chunks: 16 KB each
 constexpr int kBars = 46;                     // 8-byte words of barriers and flags
+constexpr int kMaxCluster = 8;
 constexpr float kUnset = 3.0e38f;             // minus the reference exponent before any token was seen
 constexpr float kLimit = 8.8f;                // 2^8.8 < 448: reference kept up to here
 constexpr int kListFlag = 1 << 30;            // token word: a list entry
@@ -302,9 +303,18 @@ __device__ __forceinline__ float peer_ld(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
-// All threads of the cluster: writes before are seen by reads behind it.
+// The weights warps' sums, to the producers of a block without a cluster: kWait for those that wait.
+template <int kCount, bool kWait>
+__device__ __forceinline__ void stats_barrier() {
+  if constexpr (kWait) asm volatile("barrier.cta.sync 7, %0;" ::"n"(kCount) : "memory");
+  else asm volatile("barrier.cta.arrive 7, %0;" ::"n"(kCount) : "memory");
+}
+// All threads of the cluster: writes before the arrival are seen by reads behind the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Two weights as their e4m3 codes (low half) and the e5m2 codes of what is left (high half).
@@ -411,6 +421,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The cluster's first meeting: every block's references and sums are set.  Only the weights warps
+  // have something to bring to it, and only the producers wait for it before their work is done.
+  const bool met = t.cluster > 1;
+  if (met && (warp < 4 || warp >= kMmaWarp)) cluster_arrive();
 
   if (warp < 4) {
     // ---------------------------------------------------------------- producers
@@ -907,11 +921,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         if (lane == 0) mbar_arrive(pfull);
         if (++s == pl.stages) { s = 0; ph ^= 1; }
       }
-      // The last tile's values are in.  Sums over the block's tokens, and O^T into the ring as
-      // [C][128 n_v] fp32 (every tile has been read).
-      if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
-      tc_fence_after();
-      // Each step halves the columns a lane holds; lane l ends with column l / (32 / NA).
+      // Sums over the block's tokens, while the last tile's values are made, through the info of a stage
+      // that every group has left.  Each step halves the columns a lane holds; lane l ends with
+      // column l / (32 / NA).
       float v[NA];
 #pragma unroll
       for (int c = 0; c < NA; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
@@ -927,10 +939,17 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         o >>= 1;
       }
       for (; o >= 1; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-      *scratch(quad * 32 + lane / (32 / NA)) = v[0];
+      float* sums = reinterpret_cast<float*>(info + s * kTile) + wg * 64;      // [4][NA]
+      sums[quad * NA + lane / (32 / NA)] = v[0];
       group_sync(bar_id);
       if (quad == 0 && lane < NA)
-        qf[c0 + lane] = (*scratch(lane) + *scratch(32 + lane)) + (*scratch(64 + lane) + *scratch(96 + lane));
+        qf[c0 + lane] = (sums[lane] + sums[NA + lane]) + (sums[2 * NA + lane] + sums[3 * NA + lane]);
+      __syncwarp();
+      if (met) cluster_arrive();
+      else stats_barrier<32 * Sh::kWeights + kProducers, false>();
+      // The last tile's values are in: O^T into the ring as [C][128 n_v] fp32 (every tile has been read).
+      if (ok && n > 0) ok = mbar_wait(pdone, (n - 1) & 1, abort_flag);
+      tc_fence_after();
       float* os = reinterpret_cast<float*>(ring) + row;
       const int pitch = pl.n_v * 128;
 #pragma unroll 1
@@ -953,58 +972,59 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     if (C == NC && n_c <= NC / 2) weigh(std::integral_constant<int, NC / 2>{});
     else weigh(std::integral_constant<int, NC>{});
   }
+  // ------------------------------------------------------------------ join
+  // This block's share of the columns: out = sum_x w_x O_x, w_x = 2^(r_x - r) (over the sum of
+  // the weights when the unit has one cluster).  The producers make the w_x while the last values
+  // are made and laid.
+  const int X = t.cluster, share = C >> (31 - __clz(X)), cs = rank * share;
+  float* wtab = reinterpret_cast<float*>(info);            // [X][share]: weights
+  int* place = reinterpret_cast<int*>(info) + C;           // [share]: output row of a column
+  __syncwarp();
+  if (met) cluster_wait();
+  else if (warp < 4) stats_barrier<32 * Sh::kWeights + kProducers, true>();
+  if (static_cast<int>(threadIdx.x) < share) {             // at most the first two warps
+    const int c = cs + static_cast<int>(threadIdx.x), col = c_base + c;
+    float r[kMaxCluster], l[kMaxCluster], m = -kUnset, sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      r[x] = x < X ? -peer_ld(peer(smem_u32(nref + c), x)) : 0.f;
+      l[x] = x < X ? peer_ld(peer(smem_u32(qf + c), x)) : 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x)
+      if (l[x] != 0.f) m = fmaxf(m, r[x]);
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      r[x] = l[x] != 0.f ? ex2(r[x] - m) : 0.f;
+      if (l[x] != 0.f) sum = fmaf(r[x], l[x], sum);
+    }
+    const float scale = a.splits > 1 ? 1.f : sum == 0.f ? 0.f : 1.0f / sum;
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x)
+      if (x < X) wtab[x * share + threadIdx.x] = r[x] * scale;
+    if (a.splits == 1) {
+      const int i = a.Tq == 1 ? 0 : col / hg, oc = (b * a.Tq + i) * a.H + head * hg + col - i * hg;   // at most 2^24
+      place[threadIdx.x] = oc;
+      if (a.lse && c < n_c) a.lse[oc] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+    } else {
+      const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
+      if (c < n_c) {
+        a.part_m[pc] = m;
+        a.part_l[pc] = sum;
+      }
+    }
+  }
+  __syncwarp();
   pdl_trigger();
   tc_fence_before();
-  if (t.cluster > 1) cluster_sync();
+  if (met) cluster_sync();                                 // sums and values of every block are laid
   else __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) raise_status(a.status, LSA_ERR_TIMEOUT);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  // ------------------------------------------------------------------ join
-  // This block's share of the columns: out = sum_x w_x O_x, w_x = 2^(r_x - r) (over the sum of
-  // the weights when the unit has one cluster).
   {
-    const int X = t.cluster, share = C >> (31 - __clz(X)), cs = rank * share;
-    float* wtab = reinterpret_cast<float*>(pbuf);          // [X][share]: weights
-    float2* rl = reinterpret_cast<float2*>(pbuf + C * 4);  // [X][share]: reference, sum
-    int* place = reinterpret_cast<int*>(pbuf + C * 12);    // [share]: output row (or part row) of a column
-    const int xl = 31 - __clz(X), sl = 31 - __clz(share);  // both are powers of two
-    if (threadIdx.x < C) {
-      const int x = threadIdx.x >> sl, c = cs + (threadIdx.x & (share - 1));
-      rl[threadIdx.x] = make_float2(-peer_ld(peer(smem_u32(nref + c), x)), peer_ld(peer(smem_u32(qf + c), x)));
-    }
-    __syncthreads();
-    if (threadIdx.x < share) {
-      const int c = cs + threadIdx.x, col = c_base + c;
-      float m = -kUnset, sum = 0.f;
-      for (int x = 0; x < X; ++x) {
-        const float2 v = rl[x * share + threadIdx.x];
-        if (v.y != 0.f) m = fmaxf(m, v.x);
-      }
-      for (int x = 0; x < X; ++x) {
-        const float2 v = rl[x * share + threadIdx.x];
-        if (v.y != 0.f) sum = fmaf(ex2(v.x - m), v.y, sum);
-      }
-      const float r = a.splits > 1 ? 1.f : sum == 0.f ? 0.f : 1.0f / sum;
-      for (int x = 0; x < X; ++x) {
-        const float2 v = rl[x * share + threadIdx.x];
-        wtab[x * share + threadIdx.x] = v.y != 0.f ? ex2(v.x - m) * r : 0.f;
-      }
-      if (a.splits == 1) {
-        const int i = a.Tq == 1 ? 0 : col / hg, oc = (b * a.Tq + i) * a.H + head * hg + col - i * hg;   // at most 2^24
-        place[threadIdx.x] = oc;
-        if (a.lse && c < n_c) a.lse[oc] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
-      } else {
-        const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
-        if (c < n_c) {
-          a.part_m[pc] = m;
-          a.part_l[pc] = sum;
-        }
-      }
-    }
-    __syncthreads();
     const int pitch = pl.n_v * 128, shift = a.voff - pl.v0 * 128;
     const bool vec = a.dv % 4 == 0 && shift % 4 == 0;
     const int mine = max(0, min(share, n_c - cs));
@@ -1051,10 +1071,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         }
       };
       if (p < per && v < a.dv) {
-        switch (xl) {
-          case 0: join_columns(std::integral_constant<int, 1>{}); break;
-          case 1: join_columns(std::integral_constant<int, 2>{}); break;
-          case 2: join_columns(std::integral_constant<int, 4>{}); break;
+        switch (X) {
+          case 1: join_columns(std::integral_constant<int, 1>{}); break;
+          case 2: join_columns(std::integral_constant<int, 2>{}); break;
+          case 4: join_columns(std::integral_constant<int, 4>{}); break;
           default: join_columns(std::integral_constant<int, 8>{}); break;
         }
       }
