@@ -309,7 +309,7 @@ __device__ __forceinline__ void stats_barrier() {
   if constexpr (kWait) asm volatile("barrier.cta.sync 7, %0;" ::"n"(kCount) : "memory");
   else asm volatile("barrier.cta.arrive 7, %0;" ::"n"(kCount) : "memory");
 }
-// All threads of the cluster: writes before the arrival are seen by reads behind the wait.
+// All threads of the cluster, each warp converged: writes before the arrival are seen by reads behind the wait.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -1090,7 +1090,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
     }
   }
-  if (t.cluster > 1) cluster_sync();                       // nobody reads this block's shared memory any more
+  __syncwarp();
+  if (met) cluster_sync();                                 // nobody reads this block's shared memory any more
 }
 
 // Two blocks share an SM where each gets two stages of its half; one block has it all otherwise.
