@@ -204,6 +204,7 @@ def lsa_hot_pool_update(B, N, slots, row_bytes, trigger, U, cold_host, hot, stat
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _QTYPES = (torch.float32, torch.bfloat16)
 _I32, _F32, _F64, _U8 = (torch.int32,), (torch.float32,), (torch.float64,), (torch.uint8,)
+_QTYPE = {LSA_F32: torch.float32, LSA_BF16: torch.bfloat16}
 
 
 def _bad(t, name, dtypes, n, device):
@@ -232,7 +233,9 @@ def _dev_strided(t, name, dtypes, span, device):
     view's first one must lie in its storage."""
     if t.dtype not in dtypes or t.get_device() != device or device < 0:
         raise ValueError(_bad(t, name, dtypes, 0, device))
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if 0 <= span <= t.numel() and t.is_contiguous():
+        return t.data_ptr()
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension has stride {t.stride(-1)}; it must be dense")
     if span < 0 or (t.storage_offset() + span) * t.element_size() > t.untyped_storage().nbytes():
         raise ValueError(f"{name}: {span} elements from its first one lie outside its storage")
@@ -267,7 +270,7 @@ def _kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, dev
 def lsa_kv_write(B, T, N, G, W, xdt, x, x_stride, start, count, block, page, seq_pages, pages, table, rows, scale,
                  status=None, stream=None):
     d = x.get_device()
-    if dtype_code(x) != xdt:
+    if x.dtype != _QTYPE.get(xdt):
         raise ValueError(f"x is {x.dtype}, xdt {xdt}")
     _call(lib().lsa_kv_write, "lsa_kv_write", d, stream, B, T, N, G, W, xdt,
           _dev_strided(x, "x", _QTYPES, (B * T - 1) * x_stride + G * W if B * T > 0 else 0, d), x_stride,
@@ -279,7 +282,7 @@ def lsa_kv_write(B, T, N, G, W, xdt, x, x_stride, start, count, block, page, seq
 def lsa_kv_read(B, N, G, W, idx, cap, count, block, page, seq_pages, pages, table, rows, scale, odt, out,
                 status=None, stream=None):
     d = out.get_device()
-    if dtype_code(out) != odt:
+    if out.dtype != _QTYPE.get(odt):
         raise ValueError(f"out is {out.dtype}, odt {odt}")
     _call(lib().lsa_kv_read, "lsa_kv_read", d, stream, B, N, G, W, _dev(idx, "idx", _I32, B * cap, d), cap,
           _dev(count, "count", _I32, B, d),
@@ -294,7 +297,7 @@ def lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, wi
 def lsa_kv_attend(B, Tq, N, H, G, d, dv, voff, W, qdt, q, sm_scale, length, sinks, window, idx, cap, count, block,
                   page, seq_pages, pages, table, rows, scale, out, lse, workspace, status=None, stream=None):
     dev = q.get_device()
-    if dtype_code(q) != qdt or out.dtype != q.dtype:
+    if q.dtype != _QTYPE.get(qdt) or out.dtype != q.dtype:
         raise ValueError(f"q is {q.dtype}, out {out.dtype}, qdt {qdt}")
     i32 = _I32
     _call(lib().lsa_kv_attend, "lsa_kv_attend", dev, stream, B, Tq, N, H, G, d, dv, voff, W, qdt,
@@ -308,13 +311,14 @@ def lsa_kv_attend(B, Tq, N, H, G, d, dv, voff, W, qdt, q, sm_scale, length, sink
 
 def lsa_rope(R, H, rot, half, dt, x, x_token, x_head, pos, freq, mscale, inverse, out, o_token, o_head, stream=None):
     d = x.get_device()
-    if dtype_code(x) != dt or out.dtype != x.dtype:
+    if x.dtype != _QTYPE.get(dt) or out.dtype != x.dtype:
         raise ValueError(f"x is {x.dtype}, out {out.dtype}, dt {dt}")
-    span = lambda t, h: (R - 1) * t + (H - 1) * h + rot if R > 0 and H > 0 else 0  # noqa: E731
+    some, r, h = R > 0 and H > 0, R - 1, H - 1
     _call(lib().lsa_rope, "lsa_rope", d, stream, R, H, rot, int(half), dt,
-          _dev_strided(x, "x", _QTYPES, span(x_token, x_head), d), x_token, x_head,
+          _dev_strided(x, "x", _QTYPES, r * x_token + h * x_head + rot if some else 0, d), x_token, x_head,
           _dev(pos, "pos", _I32, R, d), _dev(freq, "freq", _F64, rot // 2, d), float(mscale),
-          int(inverse), _dev_strided(out, "out", _QTYPES, span(o_token, o_head), d), o_token, o_head)
+          int(inverse), _dev_strided(out, "out", _QTYPES, r * o_token + h * o_head + rot if some else 0, d), o_token,
+          o_head)
 
 
 def lsa_rope_frequencies(rot, base=10000.0, factor=1.0, original=0.0, fast=32.0, slow=1.0) -> torch.Tensor:
