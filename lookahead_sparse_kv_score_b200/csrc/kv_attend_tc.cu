@@ -273,6 +273,7 @@ __device__ __forceinline__ void mma_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t 
 __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // L2 policy of the rows' boxes: rows that one block reads leave first (16384 tokens x 8 KV heads, B = 32:
 // 2% less time), rows that several blocks of a unit read do not.
 __device__ __forceinline__ uint64_t rows_policy(bool once) {
@@ -376,15 +377,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     u = q;
     return static_cast<int>(r);
   };
-  pdl_wait();      // what follows reads the call's inputs (by plain loads: the kernel before may have written them while this one started)
   const int rank = digit(t.cluster), cg = digit(t.col_groups), grp = digit(a.splits), head = digit(g.G);   // a.splits: clusters of a unit
   const int b = static_cast<int>(u);
   const int c_base = cg * C, n_c = min(C, ncol - c_base);
-  const KvSpan sp = kv_span(a, b);
-  const int tiles = (sp.total + kTile - 1) / kTile;
   const int parts = a.splits * t.cluster, part = grp * t.cluster + rank;
-  const int each = parts == 1 ? tiles : tiles / parts, more = tiles - each * parts;   // the first `more` parts have one tile more
-  const int tile0 = part * each + min(part, more), n = each + (part < more ? 1 : 0);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < pl.stages * pl.n_full; ++s) {
@@ -407,16 +403,33 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
-  // The query rows are on their way to L2 while the barriers are made.
+  // The kernel before may still run: what it may write is only fetched to L2 here (this part's list
+  // entries, the lengths, the query rows), and read behind the wait.
+  if (warp < 4) {
+    if (a.idx != nullptr) {
+      const long long e1 = static_cast<long long>(a.cap) * (part + 1) / parts;
+      for (long long e = static_cast<long long>(a.cap) * part / parts + threadIdx.x * 32; e < e1; e += kProducers * 32)
+        prefetch(a.idx + static_cast<size_t>(b) * a.cap + e);
+      if (threadIdx.x == 1) prefetch(a.count + b);
+    }
+    if (threadIdx.x == 0) prefetch(a.length + b);
+  }
   if (warp >= 4 && warp < kMmaWarp) {
     const int c = (warp - 4) * 4 + (lane >> 3), col = c_base + c, i = a.Tq == 1 ? 0 : col / hg;   // eight lanes a row
     if (c < n_c) {
       const char* qrow = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                        ((static_cast<size_t>(b) * a.Tq + i) * a.H + head * hg + (col - i * hg)) * a.d);
-      for (int e = (lane & 7) * 128; e < a.d * 2; e += 1024) asm volatile("prefetch.global.L2 [%0];" ::"l"(qrow + e));
+      for (int e = (lane & 7) * 128; e < a.d * 2; e += 1024) prefetch(qrow + e);
     }
   }
+  // What follows reads the call's inputs, by plain loads, and allocates tensor memory (which the kernel
+  // before may not have done yet).
+  pdl_wait();
+  if (warp == kMmaWarp) tmem_alloc(tmem_slot, kTmemCols);
+  const KvSpan sp = kv_span(a, b);
+  const int tiles = (sp.total + kTile - 1) / kTile;
+  const int each = parts == 1 ? tiles : tiles / parts, more = tiles - each * parts;   // the first `more` parts have one tile more
+  const int tile0 = part * each + min(part, more), n = each + (part < more ? 1 : 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
