@@ -38,7 +38,7 @@
 // gathers.
 //
 // What bounds it.  With few query columns, memory: 16384 tokens x 8 KV heads x 256 bytes, B = 32,
-// read at 5.5 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
+// read at 5.6 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
 // rate (an MMA of N = 128 takes 64 clocks, of N = 64 48: its operands' bytes), and the chain of a
 // tile (rows 0.9 us, S 0.6 to 1.5, weights 1.4, O 0.8 to 1.4) over the two tiles that fit beside
 // the query image comes to 2.5 to 2.8 us, against 1.7 for its bytes.  The join of a cluster is bound by
