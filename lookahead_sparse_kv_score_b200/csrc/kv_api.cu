@@ -56,7 +56,7 @@ AttendWs attend_ws(int B, int Tq, int N, int H, int G, int d, int dv, int voff, 
   AttendWs w{};
   const int ncol = Tq * (H / G);
   long long most = window < 0 ? N : std::min<long long>(N, static_cast<long long>(sinks) + window + Tq - 1);
-  most += cap + 64;                            // and the numbering's empty places
+  most += cap + (window > 0 ? 64 : 0);         // and the numbering's empty places around a window
   const int b1 = std::max(B, 1), n1 = std::max(ncol, 1);
   w.cols = N <= (1 << 30) ? kv_attend_columns_tc(b1, G, n1, most, d, dv, voff, qdt) : 0;   // token words have 30 bits
   w.cluster = 1;
