@@ -286,3 +286,19 @@ def test_read_to_any_aligned_output(dtype):
         outs.append(buf[off: off + n])
     assert (outs[0].data_ptr() % 32, outs[1].data_ptr() % 32) == (0, 16)
     assert torch.equal(outs[0], outs[1]) and (outs[0] != 5).any()
+
+
+@pytest.mark.parametrize("G,hg,d,dv,voff,W,B,N", [(1, 8, 576, 512, 0, 576, 150, 1900), (8, 5, 128, 128, 128, 256, 40, 2000),
+                                                  (2, 3, 64, 64, 64, 128, 150, 1500), (1, 9, 128, 128, 128, 256, 300, 1300)])
+def test_attend_few_columns_with_rising_weights(G, hg, d, dv, voff, W, B, N):
+    """Blocks with at most eight columns (and with one more): references that move in many tiles, for
+    some columns and for all of them, and one column that falls."""
+    c = K.Cache(13, B, N, G, W, 1, 64, "dense")
+    c.codes[..., 24] = 0x38                                            # column 24: 1.0
+    c.scale[:] = np.exp2(np.floor(np.linspace(0, 10, N)) - 6)[None, :, None]
+    c.push()
+    q = _q(3, B, 1, G * hg, d)
+    q[::2, :, :, 24] = 8.0                                             # all columns of every second sequence rise
+    q[:, :, 1, 24] = -8.0
+    q[1::4, :, 2, 24] = 12.0
+    _check(c, q, 0.02, [N - b for b in range(B)], 0, -1, None, None, d, dv, voff, _vmax(c))
