@@ -6,7 +6,7 @@
 // maximum m, the sum l and the weighted values are rescaled when a tile raises m.
 //
 // What bounds it: for short calls the latency of a tile's steps (8 columns over 64 listed tokens of
-// 576 codes, one sequence: 7.9 us; 21.8 with a warp a column and nothing read ahead); for long ones
+// 576 codes, one sequence: 8.5 us; 21.8 with a warp a column and nothing read ahead); for long ones
 // shared memory, which a column's products read at four bytes a multiply-add (16384 tokens x 16 columns,
 // B = 4: 164 us).
 //
@@ -338,7 +338,8 @@ int launch_team(const KvAttendArgs& a, cudaStream_t s) {
   const int rows_used = (std::max(a.d, a.voff + a.dv) + 15) / 16 * 16;
   const size_t smem = simt_smem(a, kTeam, rows_used);
   const auto kern = a.voff % 4 == 0 && a.dv % 4 == 0 ? kv_attend_simt_kernel<true, kTeam> : kv_attend_simt_kernel<false, kTeam>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // the largest size, not this call's: two host threads may launch different ones
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
   const long long grid = static_cast<long long>(a.g.B) * a.g.G * col_blocks * a.splits;
   kern<<<static_cast<unsigned>(grid), kWarps * 32, smem, s>>>(a, col_blocks, rows_used);

@@ -1118,7 +1118,8 @@ Plan plan_for(int d, int dv, int voff, int C) {
 
 template <int C>
 int launch_c(const CUtensorMap& map, const CUtensorMap& tail, const AttendTc& t, long long grid, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, t.p.smem);
+  // the limit, not this call's size: two host threads may launch different sizes
+  const cudaError_t e = cudaFuncSetAttribute(kv_attend_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return fail(LSA_ERR_CUDA, "kv_attend: %s", cudaGetErrorString(e));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

@@ -302,3 +302,38 @@ def test_attend_few_columns_with_rising_weights(G, hg, d, dv, voff, W, B, N):
     q[:, :, 1, 24] = -8.0
     q[1::4, :, 2, 24] = 12.0
     _check(c, q, 0.02, [N - b for b in range(B)], 0, -1, None, None, d, dv, voff, _vmax(c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_two_host_threads(dtype):
+    """Calls of two sizes from two host threads, each on its own stream: the larger one's shared memory
+    must not depend on what the other thread launches in between."""
+    import threading
+
+    work = []
+    for G, hg, d, dv, voff, W, N in [(1, 12, 576, 512, 0, 576, 400), (2, 4, 64, 64, 64, 128, 90)]:
+        c = K.Cache(d, 2, N, G, W, 16, 16, "paged")
+        q = _q(W, 2, 1, G * hg, d, dtype)
+        args = (c, q, d ** -0.5, K.i32([N, N - 7]), 0, -1, None, None, d, dv, voff)
+        want, _, _ = K.attend(*args)
+        work.append((args, want))
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(args, want):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(150):
+                    out, _, st = K.attend(*args)
+                    s.synchronize()
+                    assert torch.equal(out, want) and int(st.item()) == 0
+        except Exception as e:                                         # noqa: BLE001 (shown below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
