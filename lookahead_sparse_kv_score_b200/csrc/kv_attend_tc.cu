@@ -1138,18 +1138,28 @@ int launch_c(const CUtensorMap& map, const CUtensorMap& tail, const AttendTc& t,
   return check_launch("kv_attend");
 }
 
+// Sizes of a cluster, and the blocks resident at once (the occupancy calculator's answers on B200:
+// clusters of 4 and 8 leave some SMs of a graphics cluster unused), twice that with two blocks an SM.
+constexpr int kSizes[4] = {1, 2, 4, 8}, kRoom[4] = {148, 148, 132, 120};
+
 }  // namespace
 
 int kv_attend_columns_tc(int B, int G, int ncol, long long max_tokens, int d, int dv, int voff, int qdt) {
   // 16384 tokens a part, at most 8 parts a cluster and 256 clusters a unit
   if (qdt != LSA_BF16 || d % 8 != 0 || d > 576 || max_tokens > 16384ll * 8 * 256) return 0;
-  // The columns a block can hold; fewer where the blocks would leave SMs idle all the same: a
-  // quarter of the columns is a quarter of the sums to join (512 rows, one sequence, 64 heads:
-  // 19.7 us with 64 columns a block).
+  // The columns a block can hold; fewer where one wave of blocks takes them with four tiles a block or
+  // less all the same: a quarter of the columns is a quarter of the query image to make and of the
+  // sums to join (64 heads of latent rows: 512 rows, one sequence, 11 us with 16 columns a block, 19 with
+  // 64; 300 rows, B = 16, 13.1 against 18.4; 1000 rows, B = 8, 14.1 against 18.6).
   const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
+  auto one_wave = [&](long long units) {
+    for (int k = 0; k < 4; ++k)
+      if ((tiles + kSizes[k] - 1) / kSizes[k] <= 4 && units * kSizes[k] <= kRoom[k]) return true;
+    return false;
+  };
   for (int C = 16; C <= 64; C *= 2) {
     const bool enough = ncol <= C || C == 64;
-    if (!enough && static_cast<long long>(B) * G * ((ncol + C - 1) / C) * tiles > 148) continue;
+    if (!enough && !one_wave(static_cast<long long>(B) * G * ((ncol + C - 1) / C))) continue;
     const Plan p = plan_for(d, dv, voff, C);
     if (p.n_v <= 4 && p.stages >= 2 && p.smem <= kSmemLimit) return C;
     if (enough) return 0;
@@ -1161,22 +1171,19 @@ void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, 
   const long long units = static_cast<long long>(B) * G * ((ncol + C - 1) / C);
   const long long tiles = std::max<long long>(1, (max_tokens + kTile - 1) / kTile);
   const long long least = (max_tokens + 16383) / 16384;   // parts, by the weights' range (see the top)
-  // Blocks resident at once by cluster size (the occupancy calculator's answers on B200: clusters of
-  // 4 and 8 leave some SMs of a graphics cluster unused), twice that with two blocks an SM.
   // A division costs the tiles of a block, its start and end counted as three, times: 1.5 for
   // a block alone on an SM that could hold two, 2 for two of them, more by the waves; a second
   // kernel that joins clusters as three tiles and their sums' traffic.
-  const int xs[4] = {1, 2, 4, 8}, slots[4] = {148, 148, 132, 120};
   const double per_sm = C < 64 && plan_for(d, dv, voff, C).smem <= kSmemLimit / 2 - 1024 ? 2.0 : 1.0;
   double best = -1.0;
   for (int k = 0; k < 4; ++k) {
-    const long long X = xs[k];
+    const long long X = kSizes[k];
     if (X > 1 && X > tiles) break;
     for (long long gr = std::max<long long>(1, (least + X - 1) / X); gr <= 256; ++gr) {
       if (best >= 0.0 && X * gr > tiles) break;
-      const double blocks = static_cast<double>(units * gr * X), room = slots[k] * per_sm;
+      const double blocks = static_cast<double>(units * gr * X), room = kRoom[k] * per_sm;
       const double w = static_cast<double>((tiles + X * gr - 1) / (X * gr) + 3);
-      double c = blocks <= slots[k] ? w * (per_sm > 1.0 ? 1.5 : 1.0)
+      double c = blocks <= kRoom[k] ? w * (per_sm > 1.0 ? 1.5 : 1.0)
                  : blocks <= room ? w * 2.2
                                   : per_sm * w * (per_sm > 1.0 ? blocks / room + 0.25 : std::ceil(blocks / room));
       c += (gr > 1 ? (3.0 + gr / 16.0) * (per_sm > 1.0 ? 3.0 : 1.0) : 0.0) + 0.25 * k;
