@@ -1173,8 +1173,12 @@ void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, 
   const long long least = (max_tokens + 16383) / 16384;   // parts, by the weights' range (see the top)
   // A division costs the tiles of a block, its start and end counted as three, times: 1.5 for
   // a block alone on an SM that could hold two, 2 for two of them, more by the waves; a second
-  // kernel that joins clusters as three tiles and their sums' traffic.
-  const double per_sm = C < 64 && plan_for(d, dv, voff, C).smem <= kSmemLimit / 2 - 1024 ? 2.0 : 1.0;
+  // kernel that joins clusters as three tiles and their sums' traffic (131072 latent tokens: 45.8 us by
+  // 74 clusters of two, 46.8 by 33 of four; 20000 tokens of 256 codes, 128 columns: 21.2 and, by 16 of four,
+  // 20.0).
+  const Plan plan = plan_for(d, dv, voff, C);
+  const double per_sm = C < 64 && plan.smem <= kSmemLimit / 2 - 1024 ? 2.0 : 1.0;
+  const double traffic = plan.n_full >= 3 ? 40.0 : 16.0;   // a cluster's sums are a smaller part of a tile of wide rows
   double best = -1.0;
   for (int k = 0; k < 4; ++k) {
     const long long X = kSizes[k];
@@ -1186,7 +1190,7 @@ void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, 
       double c = blocks <= kRoom[k] ? w * (per_sm > 1.0 ? 1.5 : 1.0)
                  : blocks <= room ? w * 2.2
                                   : per_sm * w * (per_sm > 1.0 ? blocks / room + 0.25 : std::ceil(blocks / room));
-      c += (gr > 1 ? (3.0 + gr / 16.0) * (per_sm > 1.0 ? 3.0 : 1.0) : 0.0) + 0.25 * k;
+      c += (gr > 1 ? (3.0 + gr / traffic) * (per_sm > 1.0 ? 3.0 : 1.0) : 0.0) + 0.25 * k;
       if (best < 0.0 || c < best) {
         best = c;
         cluster = static_cast<int>(X);
