@@ -445,7 +445,11 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     const int n_kf = pl.n_k - pl.tail, gap = max(pl.v0 - n_kf, 0);   // chunks between keys and values are not read
     const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
     const uint64_t policy = rows_policy(t.col_groups == 1);
-    const int v_slot0 = plan_v_slot(pl, pl.v0);
+    const int v_slot0 = plan_v_slot(pl, pl.v0), v_last = v_slot0 + pl.n_v - 1;
+    // A value slot whose release says that every chunk of the stage's last tile has arrived: the scores
+    // have waited for the chunks with keys before the first values begin; chunks without keys are
+    // waited for one by one, so then it is the last.
+    const int v_done = v_last >= n_kf ? v_last : v_slot0;
     const bool divide = t.run > 0 && pl.n_full >= 3;
     const int piece = lane & 7, r_in = lane >> 3;          // a lane's 16 bytes of a chunk and its row of four
     const uint8_t* lane_base = g.rows + static_cast<size_t>(head) * g.W + piece * 16;
@@ -513,13 +517,13 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       if (divide) {
         // The stage's token words are free once the values of its last tile have begun; they carry
         // the runs' first rows to the warps.
-        if (ok) ok = mbar_wait(&empty[s * pl.n_full + v_slot0], ph ^ 1, abort_flag);
+        if (ok) ok = mbar_wait(&empty[s * pl.n_full + v_done], ph ^ 1, abort_flag);
         words[threadIdx.x].x = __int_as_float(row);
         by_chunks = !group_any(6, !runs || !ok);
       }
       if (by_chunks) {
-        // The others' chunks get nothing from this warp (their slots' last phase is over: the stage's
-        // values have begun).
+        // The others' chunks get nothing from this warp (their slots' last phase is over, by the wait
+        // for v_done).
         for (int c = 0; c < pl.n_full; ++c)
           if ((c & 3) != warp) mbar_arrive(&full[s * pl.n_full + c]);
         for (int c = warp; c < pl.n_full + pl.tail; c += 4) {
