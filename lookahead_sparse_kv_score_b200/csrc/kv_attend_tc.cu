@@ -12,21 +12,27 @@
 //
 // Rounding.  A bf16 query element has 8 significant bits; scaled by a power of two to at most
 // 448, an e4m3 term holds the first four and a second one the rest, exactly, except
-// below 2^-10 / 224 of the row's largest element.  A weight P'' (see below) is held as an e4m3
-// and an e5m2 term: half a step of each is 2^-4 * 2^-3 = 2^-7 of the weight at most (rms
-// 1.2e-3, below the bf16 rounding of the result); below 2^-6 of the unit the first term's steps
-// stop shrinking and the error is 2^-13 of the unit or an eighth of the weight, whichever is
-// less, and the e5m2 range keeps weights down to 2^-17.  The reference weight is 2^k units with
-// k = log2(tokens of the part) - 8 (0 to 6, parts of at most 16384 tokens), so the weights
-// lost below the range are less than 2^-9 of the sum.  Scores, the sum of the weights and the
-// accumulators are fp32.
+// below 2^-10 / 224 of the row's largest element.  A weight P'' (see below) is rounded to fp16 and
+// held as an e4m3 and an e5m2 term, in units that put the largest at 2^6 to 2^12.  From 2^-6
+// of a unit on, half a step of both terms is at most 2^-8 of the weight, which is what a bf16
+// weight is off by (rms 1.2e-3, a bf16 weight 1.6e-3): a second term in e5m2 leaves that much
+// behind one in e4m3, and one in e4m3 behind e5m2, which is how weights above 448 are held.  Below,
+// half a step is 2^-14 of a unit, an eighth of the weight or 2^-17 of a unit, whichever is less
+// at its size.  A heavy token that carries little value must not cost the others theirs: the unit
+// follows the tiles (see below), and in the heavy one's own tile the largest is put at 2^12, so that
+// weights keep bf16's precision down to 2^-18 of it (2^-12 where heavy tokens stand among each of
+// the four warps' shares of a tile).  Scores, the sum of the weights and the accumulators are fp32.
 //
 // Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2(scale_t); the value weight is
 // P''_tc = 2^(y_tc - r_c) and the softmax weight P''_tc / scale_t, so one exponential serves
 // both sums and the scale never multiplies the codes.  r_c is set so that the largest weight
-// seen is 2^k and kept until a weight would pass 448: then the block's O^T columns are
-// multiplied by 2^(r_old - r_new) in tensor memory.  That is rare after the first tile, so the
-// cross-lane maxima are only computed then; otherwise a tile costs one vote.
+// seen is 2^6 and kept until a weight would pass 2^12: then the block's O^T columns are
+// multiplied by 2^(r_old - r_new) in tensor memory.  (A part of one tile, and a tile in which one
+// warp's tokens all weigh far less than the largest, take 2^12 at once.)  It moves back, by up to 40
+// bits, when the tile behind a move stays below 2^-2; that tile alone is looked at, as a first
+// token of large weight, or a later one, is what makes it so.  Moves are rare after the first
+// tile, so the cross-lane maxima are only computed then; otherwise a tile costs one vote.  The room of
+// six bits is what uneven scales need: with 2^8 as the target the drafted window takes 37 us instead of 32.
 //
 // Roles (10, 14 or 22 warps by the columns).  Warps 0-3 bring the rows, one token a lane, chunk
 // by chunk, and write the tokens' scales.  Four warps for each 16 columns make the weights, one
@@ -89,7 +95,11 @@ constexpr int kMaxSlots = 12;                 // stages times 128-column chunks:
 constexpr int kBars = 46;                     // 8-byte words of barriers and flags
 constexpr int kMaxCluster = 8;
 constexpr float kUnset = 3.0e38f;             // minus the reference exponent before any token was seen
-constexpr float kLimit = 8.8f;                // 2^8.8 < 448: reference kept up to here
+constexpr float kLimit = 12.f;                // exponents of weights: reference kept up to here
+constexpr float kTarget = 6.f;                // the largest weight's when the reference is set
+constexpr float kApart = 8.f;                 // bits between two warps' largest weights that are far apart
+constexpr float kLow = -2.f;                  // the largest weight's of a tile, below which the reference may move back
+constexpr float kBack = 40.f;                 // bits that it moves back at most
 constexpr int kListFlag = 1 << 30;            // token word: a list entry
 constexpr int kAllFlag = INT_MIN;             // token word: every query of the unit sees it
 
@@ -318,12 +328,20 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_wait();
 }
 
-// Two weights as their e4m3 codes (low half) and the e5m2 codes of what is left (high half).
+// Two weights (at most 2^12) as e4m3 codes (hi) and e5m2 codes (lo) of the two terms that they are held
+// as.  Up to 448 the e4m3 term comes first and the other takes what is left; above, the e5m2 term
+// does: fp16's sign, exponent and first two fraction bits, rounded by adding half of the last
+// (the carry stays in its half: the values are far below fp16's largest), and at most 256 are left.
 __device__ __forceinline__ void split2(float2 p, uint32_t& hi, uint32_t& lo) {
-  const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
-  const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+  const __half2 w = __floats2half2_rn(p.x, p.y);
+  const uint32_t above = __hgt2_mask(w, __floats2half2_rn(448.f, 448.f));
+  const uint32_t first = (*reinterpret_cast<const uint32_t*>(&w) + 0x00800080u) & 0xff00ff00u & above;
+  const __half2 w1 = __hsub2(w, *reinterpret_cast<const __half2*>(&first));
+  const __nv_fp8x2_storage_t h = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(w1), __NV_SATFINITE, __NV_E4M3);
+  const __half2 rest = __hsub2(w1, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+  const uint32_t second = (*reinterpret_cast<const uint32_t*>(&rest) & ~above) | first;
   hi = h;
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(p.x - f.x, p.y - f.y), __NV_SATFINITE, __NV_E5M2);
+  lo = __nv_cvt_halfraw2_to_fp8x2(__half2_raw(*reinterpret_cast<const __half2*>(&second)), __NV_SATFINITE, __NV_E5M2);
 }
 
 __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[4]) {
@@ -797,8 +815,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       float2 l[NA / 2];
 #pragma unroll
       for (int c = 0; c < NA / 2; ++c) l[c] = make_float2(0.f, 0.f);
-      const float target = fminf(fmaxf(lg2(static_cast<float>(max(n, 1))) - 1.f, 0.f), 6.f);   // log2(128 n) - 8
-      bool ok = true;
+      bool ok = true, fresh = false;                         // fresh: a reference was set or moved in the tile before
+      float lowest = kUnset;                                 // of column `lane`: the smallest nref so far
       int s = 0;
       uint32_t ph = 0;
 #pragma unroll 1
@@ -857,7 +875,15 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
             float top = y[0];
 #pragma unroll
             for (int c = 1; c < NA; ++c) top = fmaxf(top, y[c]);
-            if (!group_any(bar_id, !ok || top > kLimit)) break;
+            if (group_any(bar_id, !ok || top > kLimit)) continue;
+            if (!fresh) break;
+            // Whether in each warp (that has tokens) all weights of some column are small.
+            fresh = false;
+            uint32_t high = 0;
+#pragma unroll
+            for (int c = 0; c < NA; ++c) high |= (y[c] > kLow ? 1u : 0u) << c;
+            high = __reduce_or_sync(0xffffffffu, high);
+            if (group_any(bar_id, high == (1u << NA) - 1 && __any_sync(0xffffffffu, scale != 0.f))) break;
             continue;
           }
           stop = group_any(bar_id, !ok);                     // the same for the whole group
@@ -876,8 +902,15 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
           float f_mine = 1.f, now = 0.f;
           if (lane < NA) {
             const float old = nref[c0 + lane];
-            const float m = fmaxf(fmaxf(*scratch(lane), *scratch(32 + lane)), fmaxf(*scratch(64 + lane), *scratch(96 + lane)));
-            now = m + old > kLimit ? target - m : old;
+            const float m0 = *scratch(lane), m1 = *scratch(32 + lane), m2 = *scratch(64 + lane), m3 = *scratch(96 + lane);
+            const float m01 = fmaxf(m0, m1), m23 = fmaxf(m2, m3), m = fmaxf(m01, m23);
+            // No headroom where nothing comes behind, or where the weights of some warp are all far smaller (most
+            // likely those of the next tile are too, and then the reference moves back).
+            auto seen_or = [&](float x) { return x > -INFINITY ? x : m; };
+            const float least = fminf(fminf(seen_or(m0), seen_or(m1)), fminf(seen_or(m2), seen_or(m3)));
+            const float to = (n == 1 || m - least > kApart ? kLimit : kTarget) - m;
+            now = m + old > kLimit ? to : m + old < kLow && m > -INFINITY ? fmaxf(old, fminf(to, lowest + kBack)) : old;
+            lowest = fminf(lowest, now);
             f_mine = now == old ? 1.f : ex2(now - old);      // 0 from unset
           }
           group_sync(bar_id);                                // every warp has read the old reference
@@ -885,6 +918,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
 #pragma unroll
           for (int c = 0; c < NA; ++c) (c & 1 ? l[c / 2].y : l[c / 2].x) *= __shfl_sync(0xffffffffu, f_mine, c);
           const uint32_t moved = __ballot_sync(0xffffffffu, f_mine != 1.f);   // columns whose reference moved
+          fresh = moved != 0;
           if (j > 0) {
 #pragma unroll 1
             for (int m = 0; m < pl.n_v; ++m) {
