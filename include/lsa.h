@@ -434,7 +434,10 @@ int lsa_kv_attend(int B, int Tq, int N, int H, int G, int d, int dv, int voff, i
  * lsa_rope_frequencies -- fills the HOST array freq [rot/2] with base^(-2i/rot), scaled for a
  * context `factor` times the original length by the published YaRN rule: pairs that turn more
  * than `fast` times within `original` positions keep their frequency, pairs that turn less
- * than `slow` times are divided by factor, those between blend linearly in i.  factor = 1: no
+ * than `slow` times are divided by factor, those between blend.  As in the published
+ * implementations the blend is linear in i (the paper writes it linear in the number of turns), between
+ * the numbers of the pairs, whole or not, that turn `fast` and `slow` times, rounded outwards
+ * and cut to 0 and rot - 1: its end may lie past the last pair.  factor = 1: no
  * scaling (original, fast and slow unused).  base > 1, factor >= 1, fast > slow > 0.
  * ---------------------------------------------------------------------------------- */
 int lsa_rope(int R, int H, int rot, int half, int dt, const void* x, long long x_token, long long x_head,

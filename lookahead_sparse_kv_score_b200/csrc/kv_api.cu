@@ -231,7 +231,7 @@ int lsa_rope_frequencies(int rot, double base, double factor, double original, d
     const double two_pi = 6.283185307179586476925286766559;
     auto at = [&](double turns) { return rot * std::log(original / (turns * two_pi)) / (2.0 * std::log(base)); };
     lo = std::max(std::floor(at(fast)), 0.0);
-    hi = std::min(std::ceil(at(slow)), rot / 2 - 1.0);
+    hi = std::min(std::ceil(at(slow)), rot - 1.0);   // may lie past the last pair, rot / 2 - 1
   }
   for (int i = 0; i < rot / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot);
