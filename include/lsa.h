@@ -401,7 +401,8 @@ int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const i
  *   Negative list entries are padding (as lsa_topk leaves them).  Entries at or past
  *   length[b], and visible tokens that are not resident, are skipped and raise *status to
  *   LSA_ERR_RANGE.  A token whose scale is NaN makes the queries that see it NaN; other
- *   codes and scales must be finite (codes 0x7f and 0xff are not written by lsa_kv_write).
+ *   codes and scales must be finite (codes 0x7f and 0xff are not written by lsa_kv_write).  Scales may be
+ *   0 (score 0, value 0) and negative; with bf16 queries those below 2^-60 in magnitude count as 0.
  *   d <= 576, dv <= 512, voff + dv <= 1024, H a multiple of G, B*Tq*H <= 2^24,
  *   Tq*H/G <= 65536, else LSA_ERR_UNSUPPORTED (or INVALID_ARG).
  * One launch, or two (few sequences, long ones: the parts of a sequence are joined by the second).

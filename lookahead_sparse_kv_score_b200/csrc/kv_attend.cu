@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(128) kv_attend_combine_kernel(const KvAttendAr
       if (v + e < a.dv) store_out(a.out, a.qdt, oc * a.dv + v + e, s[e] * r);
   }
   if (threadIdx.x == 0 && slice == 0 && a.lse != nullptr)
-    a.lse[oc] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+    a.lse[oc] = kv_lse(m, l);
 }
 
 size_t simt_smem(const KvAttendArgs& a, int team, int rows_used) {

@@ -23,8 +23,8 @@
 // weights keep bf16's precision down to 2^-18 of it (2^-12 where heavy tokens stand among each of
 // the four warps' shares of a tile).  Scores, the sum of the weights and the accumulators are fp32.
 //
-// Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2(scale_t); the value weight is
-// P''_tc = 2^(y_tc - r_c) and the softmax weight P''_tc / scale_t, so one exponential serves
+// Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2 |scale_t|; the value weight is
+// P''_tc = 2^(y_tc - r_c) with the scale's sign and the softmax weight P''_tc / |scale_t|, so one exponential serves
 // both sums and the scale never multiplies the codes.  r_c is set so that the largest weight
 // seen is 2^6 and kept until a weight would pass 2^12: then the block's O^T columns are
 // multiplied by 2^(r_old - r_new) in tensor memory.  (A part of one tile, and a tile in which one
@@ -100,6 +100,7 @@ constexpr float kTarget = 6.f;                // the largest weight's when the r
 constexpr float kApart = 8.f;                 // bits between two warps' largest weights that are far apart
 constexpr float kLow = -2.f;                  // the largest weight's of a tile, below which the reference may move back
 constexpr float kBack = 40.f;                 // bits that it moves back at most
+constexpr float kTiny = 0x1p-60f;             // smaller scales count as 0
 constexpr int kListFlag = 1 << 30;            // token word: a list entry
 constexpr int kAllFlag = INT_MIN;             // token word: every query of the unit sees it
 
@@ -246,6 +247,12 @@ __device__ __forceinline__ float lg2(float x) {
   float r;
   asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// log2 of a positive normal number: the exponent apart, so that a power of two's is exact (the weights are
+// divided by the scale itself: an error here would stay in them).
+__device__ __forceinline__ float log2_of(float x) {
+  const int e = static_cast<int>(__float_as_uint(x) - 0x3f800000u) >> 23;
+  return static_cast<float>(e) + lg2(__uint_as_float(__float_as_uint(x) - (static_cast<uint32_t>(e) << 23)));
 }
 __device__ __forceinline__ float warp_max(float x) {               // NaN is ignored
   float r;
@@ -488,7 +495,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       page = g.table != nullptr ? g.table[static_cast<size_t>(b) * g.n_pages + (tok >> g.page_log)] : tok >> g.page_log;
       sc = g.scale[kv_scale_at(g, b, tok, head)];
     };
-    // The token's row (-1: nothing to read), scale (0: nobody sees it) and word.
+    // The token's row (-1: nothing to read), scale (0: nobody sees it) and word.  A stored scale of 0 is a
+    // row of zeros at the smallest scale: its score is 0 and it counts among the weights.
     auto settle = [&](int tok, bool main, int page, float sc) {
       row = -1;
       scale = 0.f;
@@ -503,6 +511,10 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
       }
       row = static_cast<int>((phys << g.page_log) + (tok & ((1 << g.page_log) - 1)));
       scale = sc;
+      if (fabsf(sc) < kTiny) {
+        row = -1;
+        scale = kTiny;
+      }
       // A main token is seen by every query between two that see it; a list entry by all when it
       // lies behind every query or before every window.
       const bool all = p_first == p_last ||
@@ -826,7 +838,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         const float scale = in.x;
         const int word = __float_as_int(in.y);
         // an unseen token has scale 0: its exponent is 0 + log2(0) = -infinity
-        const float ls = scale == 0.f ? -INFINITY : lg2(scale);
+        const float ls = scale == 0.f ? -INFINITY : log2_of(fabsf(scale));
         uint32_t seen = 0xffffffffu;                         // columns of this group that see the token
         if (a.Tq > 1 && !__all_sync(0xffffffffu, word < 0 || scale == 0.f)) {
           if (word >= 0) {
@@ -947,8 +959,9 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[j & 1]);
-        // Of a NaN scale only the columns that see the token become NaN.
-        const float inv = scale > 0.f ? 1.0f / scale : 1.0f;
+        // Of a NaN scale only the columns that see the token become NaN.  A negative scale changes the codes' signs.
+        const float inv = fabsf(scale) > 0.f ? 1.0f / fabsf(scale) : 1.0f;
+        const uint32_t sign = scale < 0.f ? 0x80808080u : 0u;
         uint32_t hw[NA / 4], lw[NA / 4];
 #pragma unroll
         for (int c = 0; c < NA; c += 4) {
@@ -959,8 +972,8 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
           uint32_t h0, h1, l0, l1;
           split2(p0, h0, l0);
           split2(p1, h1, l1);
-          hw[c / 4] = h0 | (h1 << 16);
-          lw[c / 4] = l0 | (l1 << 16);
+          hw[c / 4] = (h0 | (h1 << 16)) ^ sign;
+          lw[c / 4] = (l0 | (l1 << 16)) ^ sign;
         }
         if (ok && j > 0) ok = mbar_wait(pdone, (j - 1) & 1, abort_flag);
         uint8_t* pr = pbuf + wg * 2048 + row * 16;
@@ -1056,7 +1069,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     if (a.splits == 1) {
       const int i = a.Tq == 1 ? 0 : col / hg, oc = (b * a.Tq + i) * a.H + head * hg + col - i * hg;   // at most 2^24
       place[threadIdx.x] = oc;
-      if (a.lse && c < n_c) a.lse[oc] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+      if (a.lse && c < n_c) a.lse[oc] = kv_lse(m, sum);
     } else {
       const size_t pc = ((static_cast<size_t>(b) * g.G + head) * a.splits + grp) * ncol + col;
       if (c < n_c) {

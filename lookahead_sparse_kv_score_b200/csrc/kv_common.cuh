@@ -107,6 +107,15 @@ __device__ __forceinline__ int kv_token(const KvAttendArgs& a, const KvSpan& s, 
   return e < 0 ? -1 : e;
 }
 
+// ln(2^m sum).  The exponents are added first: with scales far from 1 they are large and cancel, and a
+// rounded log2 of the whole sum would cost what the difference has.
+__device__ __forceinline__ float kv_lse(float m, float sum) {
+  if (sum == 0.f) return -INFINITY;
+  int e;
+  const float f = frexpf(sum, &e);
+  return ((m + static_cast<float>(e)) + log2f(f)) * 0.693147180559945f;
+}
+
 // The tensor-core path: query columns of a block (16, 32 or 64; 0: shape not supported), blocks
 // of a cluster and clusters of a unit (KvAttendArgs::splits).
 int kv_attend_columns_tc(int B, int G, int ncol, long long max_tokens, int d, int dv, int voff, int qdt);

@@ -110,7 +110,7 @@ def attend(c: Cache, q, sm, length, sinks, window, idx, count, d, dv, voff):
     """q [B][Tq][H][d] fp64.  Returns a dict: out [B][Tq][H][dv] and lse [B][Tq][H], and what
     tolerances need: mean = sum softmax |V| [B][Tq][H][dv]; per (b, i, h) mag = the largest
     |sm| sum |q||K| of a visible token, top = |sm| max|q| times the largest sum |K|, wide = the
-    number of visible tokens; lost = sum (min(W, 2^-17 max W) + min(W / 8, 2^-13 max W)) |V| / scale, W = softmax * scale."""
+    number of visible tokens; lost = sum (min(W, 2^-17 max W) + min(W / 8, 2^-13 max W)) |V| / scale, W = softmax * |scale|."""
     B, Tq, H, _ = q.shape
     G = c.rows.shape[2]
     r = dict(out=np.zeros((B, Tq, H, dv)), mean=np.zeros((B, Tq, H, dv)), lse=np.full((B, Tq, H), -np.inf),
@@ -142,10 +142,10 @@ def attend(c: Cache, q, sm, length, sinks, window, idx, count, d, dv, voff):
                 w = w / w.sum()
                 r["out"][b, i, h] = w @ v[:, g, voff: voff + dv]
                 r["mean"][b, i, h] = w @ np.abs(v[:, g, voff: voff + dv])
-                s = np.array([c.scale[b, t // c.block, g] for t in seen])
+                s = np.abs(np.array([c.scale[b, t // c.block, g] for t in seen]))
                 top = (w * s).max()
                 low = np.minimum(w * s, 2.0 ** -17 * top) + np.minimum(w * s / 8, 2.0 ** -13 * top)
-                r["lost"][b, i, h] = low / s @ np.abs(v[:, g, voff: voff + dv])
+                r["lost"][b, i, h] = low / np.where(s == 0, 1.0, s) @ np.abs(v[:, g, voff: voff + dv])
                 size = np.abs(v[:, g, :d])
                 r["mag"][b, i, h] = abs(sm) * (size @ np.abs(q[b, i, h])).max()
                 r["top"][b, i, h] = abs(sm) * np.abs(q[b, i, h]).max() * size.sum(1).max()
