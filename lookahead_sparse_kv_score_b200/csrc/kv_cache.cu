@@ -83,7 +83,9 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t amax) {
 // lane, at most kHold vectors and one page a block, which spares a third of the instructions
 // (0.72 are issued a cycle: 8191 tokens of 8 x 256 bf16, B = 4, blocks of 64, 182 MB, take 35.5 us,
 // 5.1 TB/s of 6.5 at the copy rate).
-template <typename T, int kWarps, bool kSimple>
+// kPages: pages are smaller than blocks of tokens, so each row is looked up (apart from the others since
+// its code alone costs one token's write 0.4 us).
+template <typename T, int kWarps, bool kSimple, bool kPages>
 __global__ void __launch_bounds__(kThreads, 4)
 kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __restrict__ x, size_t x_stride, int lpr,
                 const int32_t* __restrict__ start, const int32_t* __restrict__ count, int32_t* status) {
@@ -143,11 +145,24 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
         next_x(left, p);
       }
     }
+  // Tokens that are not resident are skipped and have no part in the scale.
+  const int t_new = static_cast<int>(first) + lo;    // the team's first token
+  bool some = false;
+  if constexpr (kPages) {
+    bool away = false, here = false;
+    for (int i = lane; i < rows; i += 32) (kv_row(g, b, t_new + i) < 0 ? away : here) = true;
+    some = __any_sync(0xffffffffu, away);
+    if (some) raise_status(status, LSA_ERR_RANGE);
+    if (!__any_sync(0xffffffffu, here)) return;      // the whole team
+  }
+  auto counts = [&](int k) {                         // whether the row of the k-th vector does
+    return !kPages || !some || kv_row(g, b, t_new + row0 + ((k % nr) << step_log)) >= 0;
+  };
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
-    if (k < nv) m = max(m, amax_bits(held[k]));
+    if (k < nv && counts(k)) m = max(m, amax_bits(held[k]));
   for (int k = kHold; !kSimple && k < nv; ++k) {
-    m = max(m, amax_bits(load8(p)));
+    if (counts(k)) m = max(m, amax_bits(load8(p)));
     next_x(left, p);
   }
   m = __reduce_max_sync(0xffffffffu, m);
@@ -167,26 +182,33 @@ kv_write_kernel(const KvGeom g, int n_new, uint32_t blocks_per_seq, const T* __r
   const float s = __uint_as_float(sb);
   const bool finite = sb != kNanBits;
   const float inv = finite ? 1.0f / s : 0.f;
+  if (kPages && grown_block && !(before == s) && (finite || before == before)) {
+    // The scale changes, which an earlier token that is not resident cannot follow: all stays as it is.
+    bool away = false;
+    for (long long t = t0 + lane; t < first; t += 32) away |= kv_row(g, b, static_cast<int>(t)) < 0;
+    if (__any_sync(0xffffffffu, away)) {
+      raise_status(status, LSA_ERR_RANGE);
+      return;
+    }
+  }
+  const long long place0 = kPages ? 0 : kv_row(g, b, t_new);
+  if (place0 < 0) {
+    raise_status(status, LSA_ERR_RANGE);
+    return;
+  }
   if (lane == 0 && team_warp == 0) *sp = s;
 
-  // A block of tokens lies in one page unless pages are smaller; then each row is looked up.
-  const bool one_page = g.page_log >= g.block_log;
   const size_t row_bytes = static_cast<size_t>(g.G) * g.W;
   uint8_t* const base = g.rows + static_cast<size_t>(head) * g.W + col0 * 8;
-  const int t_new = static_cast<int>(first) + lo;    // the team's first token
-  const long long place0 = one_page ? kv_row(g, b, t_new) : 0;
-  if (one_page && place0 < 0) {
-    raise_status(status, LSA_ERR_RANGE);
-  } else {
+  {
     uint8_t* dst = base + static_cast<size_t>(place0 + row0) * row_bytes;
     const size_t d_step = row_bytes << step_log;
     int r = row0, col = 0;
     auto put = [&](const Raw& raw) {
       bool there = true;
-      if (!one_page) {
+      if constexpr (kPages) {
         const long long place = kv_row(g, b, t_new + r);
         there = place >= 0;
-        if (!there) raise_status(status, LSA_ERR_RANGE);
         dst = base + static_cast<size_t>(there ? place : 0) * row_bytes + col;
       }
       if (there) {
@@ -368,17 +390,19 @@ void write_typed(const KvGeom& g, int n_new, int per_seq, const void* x, size_t 
   // A warp takes a unit whose vectors its lanes can hold, a block of eight warps a larger one.
   const int per_lane = ((rows << lpr) + 31) / 32 * ((vpr + 31) / 32);
   const int hold = sizeof(T) == 2 ? 9 : 5, team_lane = ((rows << lpr) + 255) / 256;   // vectors a lane of eight warps, one column
-  const bool simple = vpr <= 32 && g.page_log >= g.block_log;
+  const bool simple = vpr <= 32;
   const unsigned small = static_cast<unsigned>((units + 7) / 8), large = static_cast<unsigned>(units);
   const T* xt = static_cast<const T*>(x);
-  if (per_lane <= hold && simple)
-    kv_write_kernel<T, 1, true><<<small, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
-  else if (per_lane <= hold)
-    kv_write_kernel<T, 1, false><<<small, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
-  else if (team_lane <= hold && simple)
-    kv_write_kernel<T, 8, true><<<large, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
-  else
-    kv_write_kernel<T, 8, false><<<large, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
+  const bool pages = g.page_log < g.block_log;
+  auto launch = [&](auto kern, unsigned grid) {
+    kern<<<grid, kThreads, 0, s>>>(g, n_new, per_seq, xt, x_stride, lpr, start, count, status);
+  };
+  if (per_lane <= hold) {
+    launch(pages ? kv_write_kernel<T, 1, false, true> : simple ? kv_write_kernel<T, 1, true, false> : kv_write_kernel<T, 1, false, false>, small);
+  } else {
+    launch(pages ? kv_write_kernel<T, 8, false, true>
+                 : team_lane <= hold && simple ? kv_write_kernel<T, 8, true, false> : kv_write_kernel<T, 8, false, false>, large);
+  }
 }
 
 }  // namespace

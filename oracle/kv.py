@@ -57,7 +57,9 @@ class Cache:
 
 
 def write(c: Cache, x, start, count):
-    """x [B][T][G][W] fp64; updates c.rows and c.scale.  True when a token was skipped."""
+    """x [B][T][G][W] fp64; updates c.rows and c.scale.  True when a token was skipped: outside the
+    cache, of a sequence that starts below 0, not resident, or in a block whose scale would change while
+    an earlier token of it is not resident."""
     skipped = False
     B, T, G, W = x.shape
     for b in range(B):
@@ -66,23 +68,25 @@ def write(c: Cache, x, start, count):
         if new and int(start[b]) < 0:
             continue
         new = {t: v for t, v in new.items() if 0 <= t < c.N}
-        for j in sorted({t // c.block for t in new}):
-            mine = [t for t in new if t // c.block == j]
+        here = {t: v for t, v in new.items() if c.place(b, t) is not None}
+        skipped |= len(here) < len(new)
+        for j in sorted({t // c.block for t in here}):
+            mine = [t for t in here if t // c.block == j]
             old = list(range(j * c.block, int(start[b])))
+            away = any(c.place(b, t) is None for t in old)
             for g in range(G):
                 amax = max((math.inf if not np.isfinite(new[t][g]).all() else float(np.abs(new[t][g]).max()))
                            for t in mine)
                 s, before = block_scale(amax), float(c.scale[b, j, g])
                 if old:
                     s = math.nan if math.isnan(s) or not math.isfinite(before) else max(s, before)
+                    if away and not (s == before or math.isnan(s) and math.isnan(before)):
+                        skipped = True
+                        continue
                 c.scale[b, j, g] = s
                 ok = not math.isnan(s)
                 for t in mine:
-                    at = c.place(b, t)
-                    if at is None:
-                        skipped = True
-                        continue
-                    c.rows[at][g] = e4m3_code(e4m3_round(new[t][g] / s)) if ok else 0
+                    c.rows[c.place(b, t)][g] = e4m3_code(e4m3_round(new[t][g] / s)) if ok else 0
                 for t in old:
                     at = c.place(b, t)
                     if at is None or s == before:
