@@ -361,12 +361,13 @@ int lsa_hot_pool_update(int B, int N, int slots, size_t row_bytes, uint32_t trig
  * their codes.  A block with a NaN or infinity gets the scale NaN and codes 0.
  *   x: xdt (LSA_F32 or LSA_BF16), token (b, i) at element (b*T + i) * x_stride, [G][W] dense;
  *   16-byte aligned, x_stride a multiple of 16 bytes.  start, count [B] int32.
- *   Tokens outside [0, N) or not resident are skipped, have no part in a scale, and raise *status (int32 or
- *   NULL) to LSA_ERR_RANGE.  So do, for each head, the new tokens of a block whose scale would change
- *   while an earlier token of it is not resident (pages smaller than blocks): its codes could not follow,
- *   and that head's block stays as it was.  A sequence whose start is negative is an inactive one: with
- *   new tokens it is skipped whole and raises *status.  No two sequences may write the same page or share a partly filled block's
- *   pages.  One launch.  B * T * G < 2^30.
+ *   Tokens outside [0, N) or not resident are skipped, have no part in a scale, and raise *status
+ *   (int32 or NULL) to LSA_ERR_RANGE.  So do, for each head, the new tokens of a block whose scale
+ *   would change while an earlier token of it is not resident (pages smaller than blocks): its codes
+ *   could not follow, and that head's block stays as it was.  A sequence whose start is negative is
+ *   an inactive one: with new tokens it is skipped whole and raises *status.
+ *   No two sequences may write the same page or share a partly filled block's pages.  One launch.
+ *   B * T * G < 2^30.
  *
  * lsa_kv_read -- reads tokens back: out[b][j] = the values [G][W] of token idx[b][j] (token j
  * itself when idx is NULL, then cap <= N), j < count[b] (all cap when count is NULL).

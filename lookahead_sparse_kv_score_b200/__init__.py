@@ -228,17 +228,43 @@ def _dev(t, name, dtypes, n, device):
     raise ValueError(_bad(t, name, dtypes, n, device))
 
 
-def _dev_strided(t, name, dtypes, span, device):
+def _runs(counts, strides):
+    """(count, stride) of a nest of dimensions, the innermost first, those that continue one another as one."""
+    runs = []
+    for n, s in zip(reversed(counts), reversed(strides)):
+        if n == 1:
+            continue
+        if runs and runs[-1][0] * runs[-1][1] == s:
+            runs[-1] = (runs[-1][0] * n, runs[-1][1])
+        else:
+            runs.append((n, s))
+    return runs
+
+
+def _same_walk(t, counts, strides):
+    """Whether the view's first elements, in its own order, are those that `counts` steps of
+    `strides` meet (outermost first)."""
+    view, call = _runs(t.shape, t.stride()), _runs(counts, strides)
+    for k, (n, s) in enumerate(call):
+        if k >= len(view) or view[k][1] != s or view[k][0] < n or (view[k][0] > n and k + 1 < len(call)):
+            return False
+    return True
+
+
+def _dev_strided(t, name, dtypes, span, device, counts=None, strides=None):
     """As _dev for a view that the call walks with strides of its own: `span` elements from the
-    view's first one must lie in its storage."""
+    view's first one must lie in its storage, and a view that is not dense must have the elements that
+    the call meets (counts and strides of its dimensions, outermost first)."""
     if t.dtype not in dtypes or t.get_device() != device or device < 0:
         raise ValueError(_bad(t, name, dtypes, 0, device))
-    if 0 <= span <= t.numel() and t.is_contiguous():
+    if 0 <= span <= t.numel() and t.is_contiguous() or t.shape == counts and t.stride() == strides and span >= 0:
         return t.data_ptr()
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension has stride {t.stride(-1)}; it must be dense")
     if span < 0 or (t.storage_offset() + span) * t.element_size() > t.untyped_storage().nbytes():
         raise ValueError(f"{name}: {span} elements from its first one lie outside its storage")
+    if counts is not None and span and not t.is_contiguous() and not _same_walk(t, counts, strides):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} has strides {t.stride()}, the call walks {counts} by {strides}")
     return t.data_ptr()
 
 
@@ -273,7 +299,8 @@ def lsa_kv_write(B, T, N, G, W, xdt, x, x_stride, start, count, block, page, seq
     if x.dtype != _QTYPE.get(xdt):
         raise ValueError(f"x is {x.dtype}, xdt {xdt}")
     _call(lib().lsa_kv_write, "lsa_kv_write", d, stream, B, T, N, G, W, xdt,
-          _dev_strided(x, "x", _QTYPES, (B * T - 1) * x_stride + G * W if B * T > 0 else 0, d), x_stride,
+          _dev_strided(x, "x", _QTYPES, (B * T - 1) * x_stride + G * W if B * T > 0 else 0, d, (B * T, G * W), (x_stride, 1)),
+          x_stride,
           _dev(start, "start", _I32, B, d), _dev(count, "count", _I32, B, d),
           *_kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, d),
           _dev(status, "status", _I32, 1, d))
@@ -315,10 +342,11 @@ def lsa_rope(R, H, rot, half, dt, x, x_token, x_head, pos, freq, mscale, inverse
         raise ValueError(f"x is {x.dtype}, out {out.dtype}, dt {dt}")
     some, r, h = R > 0 and H > 0, R - 1, H - 1
     _call(lib().lsa_rope, "lsa_rope", d, stream, R, H, rot, int(half), dt,
-          _dev_strided(x, "x", _QTYPES, r * x_token + h * x_head + rot if some else 0, d), x_token, x_head,
+          _dev_strided(x, "x", _QTYPES, r * x_token + h * x_head + rot if some else 0, d, (R, H, rot), (x_token, x_head, 1)),
+          x_token, x_head,
           _dev(pos, "pos", _I32, R, d), _dev(freq, "freq", _F64, rot // 2, d), float(mscale),
-          int(inverse), _dev_strided(out, "out", _QTYPES, r * o_token + h * o_head + rot if some else 0, d), o_token,
-          o_head)
+          int(inverse), _dev_strided(out, "out", _QTYPES, r * o_token + h * o_head + rot if some else 0, d, (R, H, rot),
+                                   (o_token, o_head, 1)), o_token, o_head)
 
 
 def lsa_rope_frequencies(rot, base=10000.0, factor=1.0, original=0.0, fast=32.0, slow=1.0) -> torch.Tensor:
