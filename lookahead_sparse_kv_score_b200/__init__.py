@@ -317,8 +317,14 @@ def lsa_kv_read(B, N, G, W, idx, cap, count, block, page, seq_pages, pages, tabl
           _dev(out, "out", _QTYPES, B * cap * G * W, d), _dev(status, "status", _I32, 1, d))
 
 
+def _clip32(n):
+    """n, or the nearest 32-bit number (a C int would take the low bits): for counts of tokens that may
+    be larger than any sequence."""
+    return n if -0x80000000 <= n <= 0x7FFFFFFF else 0x7FFFFFFF if n > 0 else -0x80000000
+
+
 def lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, window, cap) -> int:
-    return int(lib().lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, sinks, window, cap))
+    return int(lib().lsa_kv_attend_workspace_bytes(B, Tq, N, H, G, d, dv, voff, W, qdt, _clip32(sinks), _clip32(window), cap))
 
 
 def lsa_kv_attend(B, Tq, N, H, G, d, dv, voff, W, qdt, q, sm_scale, length, sinks, window, idx, cap, count, block,
@@ -328,8 +334,8 @@ def lsa_kv_attend(B, Tq, N, H, G, d, dv, voff, W, qdt, q, sm_scale, length, sink
         raise ValueError(f"q is {q.dtype}, out {out.dtype}, qdt {qdt}")
     i32 = _I32
     _call(lib().lsa_kv_attend, "lsa_kv_attend", dev, stream, B, Tq, N, H, G, d, dv, voff, W, qdt,
-          _dev(q, "q", _QTYPES, B * Tq * H * d, dev), float(sm_scale), _dev(length, "length", i32, B, dev), sinks,
-          window, _dev(idx, "idx", i32, B * cap, dev), cap, _dev(count, "count", i32, B, dev),
+          _dev(q, "q", _QTYPES, B * Tq * H * d, dev), float(sm_scale), _dev(length, "length", i32, B, dev), _clip32(sinks),
+          _clip32(window), _dev(idx, "idx", i32, B * cap, dev), cap, _dev(count, "count", i32, B, dev),
           *_kv_cache(B, N, G, W, block, page, seq_pages, pages, table, rows, scale, dev),
           _dev(out, "out", _QTYPES, B * Tq * H * dv, dev), _dev(lse, "lse", _F32, B * Tq * H, dev),
           _dev(status, "status", i32, 1, dev), _dev(workspace, "workspace", _U8, 0, dev),

@@ -1,5 +1,7 @@
-"""Views whose own strides are not the ones that the call walks are refused (host tensors that pass for
-device ones; nothing is launched)."""
+"""What the binding passes on: views whose own strides are not the ones that the call walks are refused,
+and numbers past 32 bits are not cut (host tensors that pass for device ones; nothing is launched)."""
+import sys
+
 import pytest
 import torch
 
@@ -74,3 +76,18 @@ def test_calls_pass_their_walks(monkeypatch):
         with pytest.raises(ValueError, match="walks"):
             lsa.lsa_rope(4, 2, 16, 0, 0, part, *x_s, i, freq, 1.0, 0, o, *((32, 16) if o is out else (64, 32)))
     assert seen == ["lsa_kv_write", "lsa_rope"]
+
+
+@pytest.mark.parametrize("given,passed", [(2 ** 32, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (sys.maxsize, 2 ** 31 - 1),
+                                          (2 ** 31 - 1, 2 ** 31 - 1), (7, 7), (0, 0), (-1, -1), (-2 ** 40, -2 ** 31)])
+def test_windows_past_32_bits(monkeypatch, given, passed):
+    seen = []
+    monkeypatch.setattr(lsa, "_call", lambda fn, where, device, stream, *args: seen.append(args))
+    size = (1, 1, 64, 2, 1, 32, 32, 0, 32)
+    q, out, i = _view(1, 1, 2, 32), _view(1, 1, 2, 32), torch.zeros(64, dtype=torch.int32).as_subclass(Fake)
+    rows, scale = torch.zeros(2048, dtype=torch.uint8).as_subclass(Fake), torch.zeros(64).as_subclass(Fake)
+    lsa.lsa_kv_attend(*size, 0, q, 1.0, i, max(given, 0), given, None, 0, None, 1, 1, 64, 64, None, rows, scale, out, None, rows)
+    at = len(size) + 4
+    assert seen[0][at: at + 2] == (max(passed, 0), passed)
+    assert lsa.lsa_kv_attend_workspace_bytes(*size, 0, max(given, 0), given, 0) == \
+        lsa.lsa_kv_attend_workspace_bytes(*size, 0, max(passed, 0), passed, 0)
