@@ -21,7 +21,9 @@
 // at its size.  A heavy token that carries little value must not cost the others theirs: the unit
 // follows the tiles (see below), and in the heavy one's own tile the largest is put at 2^12, so that
 // weights keep bf16's precision down to 2^-18 of it (2^-12 where heavy tokens stand among each of
-// the four warps' shares of a tile).  Scores, the sum of the weights and the accumulators are fp32.
+// the four warps' shares of a tile).  Parts have at most 16384 tokens, so that the weights lost below
+// 2^-17 of a unit are less than 2^-9 of the sum.  Scores, the sum of the weights and the accumulators
+// are fp32.
 //
 // Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2 |scale_t|; the value weight is
 // P''_tc = 2^(y_tc - r_c) with the scale's sign and the softmax weight P''_tc / |scale_t|, so one exponential serves
@@ -44,7 +46,7 @@
 // gathers.
 //
 // What bounds it.  With few query columns, memory: 16384 tokens x 8 KV heads x 256 bytes, B = 32,
-// read at 5.6 TB/s.  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
+// read at 5.6 TB/s (146.8 us).  With 64 columns on latent rows a tile's products take 1.4 us at shared memory's
 // rate (an MMA of N = 128 takes 64 clocks, of N = 64 48: its operands' bytes), and the chain of a
 // tile (rows 0.9 us, S 0.6 to 1.5, weights 1.4, O 0.8 to 1.4) over the two tiles that fit beside
 // the query image comes to 2.5 to 2.8 us, against 1.7 for its bytes.  The join of a cluster is bound by
@@ -818,7 +820,7 @@ kv_attend_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_consta
     }
     // NA: 16 (NC), or 8 where the block has no more columns (what lies behind is not read): 16384 tokens x 8 KV
     // heads of 8 columns, B = 32, take 147 us, 154 with 16.  One group of several on its own code is
-    // slower (20 columns, 4096 tokens x 7 heads, B = 8: 33.6 us, 31.1 with 16 in both).
+    // slower (20 columns, 4096 tokens x 7 heads, B = 8: by 2.5 us).
     auto weigh = [&](auto active) {
       constexpr int NA = decltype(active)::value;
       // Scratch of 512 words for the group, in its own columns' block of the weights buffer, while no
@@ -1224,8 +1226,8 @@ void kv_attend_parts_tc(int B, int G, int ncol, int C, int d, int dv, int voff, 
   const long long least = (max_tokens + 16383) / 16384;   // parts, by the weights' range (see the top)
   // A division costs the tiles of a block, its start and end counted as three, times: 1.5 for
   // a block alone on an SM that could hold two, 2 for two of them, more by the waves; a second
-  // kernel that joins clusters as three tiles and their sums' traffic (131072 latent tokens: 45.8 us by
-  // 74 clusters of two, 46.8 by 33 of four; 20000 tokens of 256 codes, 128 columns: 21.2 and, by 16 of four,
+  // kernel that joins clusters as three tiles and their sums' traffic (131072 latent tokens: 47.4 us by
+  // 74 clusters of two, 1.0 more by 33 of four; 20000 tokens of 256 codes, 128 columns: 21.2 and, by 16 of four,
   // 20.0).
   const Plan plan = plan_for(d, dv, voff, C);
   const double per_sm = C < 64 && plan.smem <= kSmemLimit / 2 - 1024 ? 2.0 : 1.0;

@@ -315,9 +315,10 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) 
 // A warp reads 2^tpw_log listed tokens.  Its lanes look the tokens up first (list entry, page and,
 // with one head, scale; the list's entry does not wait for the count), then take the tokens'
 // rows together, kFlight vectors a lane in flight.  kWide: 16 codes a lane (32 bytes of bf16 out in
-// one store) where the output's alignment allows it, else eight.  Bound by memory: 100 MB of
-// random 576-byte rows and their bf16 take 22.6 us (4.4 TB/s; 23.5 with eight codes a lane),
-// of 15.3 at the copy rate; more vectors in flight, or all 64 warps on an SM, change nothing.
+// one store) where the output's alignment allows it, else eight.  100 MB of listed 576-byte rows and
+// their bf16 take 21.7 us (4.6 TB/s, 15.3 us at the copy rate; 23.5 with eight codes a lane), random rows
+// as consecutive ones; more vectors in flight, or all 64 warps on an SM, change nothing.  What is left is the
+// two dependent loads before a warp's rows, and that two thirds of the bytes are stores.
 template <typename T, bool kWide>
 __global__ void __launch_bounds__(kThreads)
 kv_read_kernel(const KvGeom g, const int32_t* __restrict__ idx, int cap, const int32_t* __restrict__ count,
@@ -418,8 +419,8 @@ int launch_kv_write(const KvGeom& g, int T, int xdt, const void* x, size_t x_str
 
 int launch_kv_read(const KvGeom& g, const int32_t* idx, int cap, const int32_t* count, int odt, void* out,
                    int32_t* status, cudaStream_t s) {
-  // As many tokens a warp (up to 4) as leave 64 warps for each SM (those rows: 22.6 us with 4 tokens a
-  // warp and with 8, 25.4 with 2).
+  // As many tokens a warp (up to 4) as leave 64 warps for each SM (those rows: the same with 4 tokens a
+  // warp and with 8, 2.8 us more with 2).
   int tpw = 0;
   while (tpw < 2 && (static_cast<long long>(g.B) * cap >> (tpw + 1)) >= 64 * 148) ++tpw;
   const long long per_seq = (cap + (1ll << tpw) - 1) >> tpw, warps = per_seq * g.B;
