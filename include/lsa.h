@@ -398,8 +398,10 @@ int lsa_kv_read(int B, int N, int G, int W, const int32_t* idx, int cap, const i
  * A query that sees nothing gets out = 0 and lse = -infinity.  Latent rows have keys and
  * values in the same columns (voff = 0); rows with separate parts have voff = d.
  * Scores, sums and lse are fp32.  With bf16 queries the weights that multiply the values are held to
- * bf16's precision (half a step 2^-8 of themselves) wherever they are at least 2^-12 of the largest
- * of their 128 tokens, whatever the others weigh; far smaller ones are coarser.
+ * bf16's precision (half a step 2^-8 of themselves) down to 2^-12 of the largest weight before them;
+ * a token that stands alone far above (a first token that takes almost all of the weight) is left
+ * out of that, but for the 128 tokens around it, which keep the precision down to 2^-18 of its weight.
+ * Smaller weights are coarser.
  *   q [B][Tq][H][d] and out [B][Tq][H][dv]: qdt (LSA_F32 or LSA_BF16); length, count [B]
  *   int32; lse [B][Tq][H] fp32 or NULL; 0 <= length[b] <= N (clamped).
  *   Negative list entries are padding (as lsa_topk leaves them).  Entries at or past

@@ -10,31 +10,32 @@
 // With tokens as M in the first product and value columns as M in the second, a few query
 // columns cost a few columns of N instead of a padded M.
 //
-// Rounding.  A bf16 query element has 8 significant bits; scaled by a power of two to at most
-// 448, an e4m3 term holds the first four and a second one the rest, exactly, except
-// below 2^-10 / 224 of the row's largest element.  A weight P'' (see below) is rounded to fp16 and
-// held as an e4m3 and an e5m2 term, in units that put the largest at 2^6 to 2^12.  From 2^-6
-// of a unit on, half a step of both terms is at most 2^-8 of the weight, which is what a bf16
-// weight is off by (rms 1.2e-3, a bf16 weight 1.6e-3): a second term in e5m2 leaves that much
-// behind one in e4m3, and one in e4m3 behind e5m2, which is how weights above 448 are held.  Below,
-// half a step is 2^-14 of a unit, an eighth of the weight or 2^-17 of a unit, whichever is less
-// at its size.  A heavy token that carries little value must not cost the others theirs: the unit
-// follows the tiles (see below), and in the heavy one's own tile the largest is put at 2^12, so that
-// weights keep bf16's precision down to 2^-18 of it (2^-12 where heavy tokens stand among each of
-// the four warps' shares of a tile).  Parts have at most 16384 tokens, so that the weights lost below
-// 2^-17 of a unit are less than 2^-9 of the sum.  Scores, the sum of the weights and the accumulators
-// are fp32.
+// Rounding.  A bf16 query element has 8 significant bits; scaled by a power of two to at most 448,
+// an e4m3 term holds the first four and a second one the rest, exactly, except below 2^-10 / 224 of
+// the row's largest element.  A weight P'' (see below) is rounded to fp16 and held as an e4m3 and
+// an e5m2 term, in units that put the largest at 2^6 to 2^12.  From 2^-6 of a unit on, half a step
+// of both terms is at most 2^-8 of the weight, which is what a bf16 weight is off by (rms 1.2e-3, a
+// bf16 weight 1.6e-3): a second term in e5m2 leaves that much behind one in e4m3, and one in e4m3
+// behind e5m2, which is how weights above 448 are held.  Below, half a step is 2^-14 of a unit, an
+// eighth of the weight or 2^-17 of a unit, whichever is less at its size: so weights keep bf16's
+// precision down to 2^-12 of the largest before them.  A heavy token that carries little value must
+// not cost the others theirs: the unit moves back behind it (see below), and in its own tile the
+// largest is put at 2^12, so that the precision reaches down to 2^-18 of it (2^-12 where heavy
+// tokens stand among each of the four warps' shares of a tile).  Parts have at most 16384 tokens,
+// so that the weights lost below 2^-17 of a unit are less than 2^-9 of the sum.  Scores, the sum of
+// the weights and the accumulators are fp32.
 //
-// Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2 |scale_t|; the value weight is
-// P''_tc = 2^(y_tc - r_c) with the scale's sign and the softmax weight P''_tc / |scale_t|, so one exponential serves
-// both sums and the scale never multiplies the codes.  r_c is set so that the largest weight
-// seen is 2^6 and kept until a weight would pass 2^12: then the block's O^T columns are
-// multiplied by 2^(r_old - r_new) in tensor memory.  (A part of one tile, and a tile in which one
-// warp's tokens all weigh far less than the largest, take 2^12 at once.)  It moves back, by up to 40
-// bits, when the tile behind a move stays below 2^-2; that tile alone is looked at, as a first
-// token of large weight, or a later one, is what makes it so.  Moves are rare after the first
-// tile, so the cross-lane maxima are only computed then; otherwise a tile costs one vote.  The room of
-// six bits is what uneven scales need: with 2^8 as the target the drafted window takes 37 us instead of 32.
+// Scales.  y_tc = sm log2(e) scale_t (q_c . k_t) + log2 |scale_t|; the value weight is P''_tc =
+// 2^(y_tc - r_c) with the scale's sign and the softmax weight P''_tc / |scale_t|, so one
+// exponential serves both sums and the scale never multiplies the codes.  r_c is set so that the
+// largest weight seen is 2^6 and kept until a weight would pass 2^12: then the block's O^T columns
+// are multiplied by 2^(r_old - r_new) in tensor memory.  (A part of one tile, and a tile in which
+// one warp's tokens all weigh far less than the largest, take 2^12 at once.)  It moves back, by up
+// to 40 bits, when the tile behind a move stays below 2^-2; that tile alone is looked at, as a
+// first token of large weight, or a later one, is what makes it so.  Moves are rare after the first
+// tile, so the cross-lane maxima are only computed then; otherwise a tile costs one vote.  The room
+// of six bits is what uneven scales need: with 2^8 as the target the drafted window takes 37 us
+// instead of 32.
 //
 // Roles (10, 14 or 22 warps by the columns).  Warps 0-3 bring the rows, one token a lane, chunk
 // by chunk, and write the tokens' scales.  Four warps for each 16 columns make the weights, one
